@@ -16,14 +16,16 @@ LIB_PATH = os.path.join(HERE, "libgrz.so")
 GRZ_OK, GRZ_EINVAL, GRZ_EINDIVISIBLE, GRZ_EALIGN, GRZ_EHIP, GRZ_ERANGE = range(6)
 GRZ_F32, GRZ_BF16, GRZ_F64 = 0, 1, 2
 (GRZ_SUM, GRZ_UNEVEN, GRZ_IN_COMPACT, GRZ_BF16_WIRE, GRZ_IN_RANGE, GRZ_ARGS_DEVICE,
- GRZ_OUT_GLOBAL, GRZ_IN_TILED, GRZ_MEAN_BF16, GRZ_COOPERATIVE) = (1, 2, 4, 8, 16, 32, 64, 128,
-                                                                 256, 512)
+ GRZ_OUT_GLOBAL, GRZ_IN_TILED, GRZ_MEAN_BF16, GRZ_COOPERATIVE,
+ GRZ_ACCUMULATE) = (1, 2, 4, 8, 16, 32, 64, 128, 256, 512, 1024)
 GRZ_MAX_RANKS = 16
 GRZ_PIECE = 4096
 GRZ_NOALLOC_SCRATCH_BYTES = 65536
+GRZ_MAX_TOP = 128
 
 # Every symbol include/grz.h declares, with (restype, argtypes).
 _vp, _i, _i64, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_double
+_f = ctypes.c_float
 _pp = ctypes.POINTER(ctypes.c_void_p)
 
 
@@ -72,6 +74,17 @@ SIGNATURES = {
                               _vp]),
     "zero1_fused_step_args": (_i, [_pp, _i, _i, _BP, _i, _i, _i, _vp, _vp, _vp, _vp, _i64, _vp,
                                    _vp, _d, _pp, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "dp_embed_lookup": (_i, [_vp, _i, _i64, _i64, _i64, _vp, _i, _i64, _f, _vp, _i, _i64, _vp]),
+    "dp_embed_grad_workspace": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "dp_embed_grad": (_i, [_vp, _i, _i64, _vp, _i, _i64, _i64, _i64, _f, _i, _vp, _vp, _i, _i64,
+                           _vp]),
+    "dp_token_logprobs": (_i, [_vp, _i, _i64, _i64, _i64, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "dp_token_logprobs_grad": (_i, [_vp, _i, _i64, _i64, _i64, _vp, _i, _vp, _vp, _vp, _vp, _vp,
+                                    _i64, _vp]),
+    "dp_distill_loss": (_i, [_vp, _i, _i64, _i64, _i64, _vp, _i, _vp, _i, _i, _f, _vp, _vp,
+                             _vp]),
+    "dp_distill_grad": (_i, [_vp, _i, _i64, _i64, _i64, _vp, _i, _vp, _i, _i, _f, _vp, _f, _vp,
+                             _vp, _i64, _vp]),
 }
 
 _lib = None

@@ -6,6 +6,7 @@ on its own and ``-fhip-fp32-correctly-rounded-divide-sqrt`` keeps fp32
 division and square root IEEE-exact; packed fp32 instructions are switched off.
 """
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
@@ -14,6 +15,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "grz.hip")
+TOKENS_SRC = os.path.join(HERE, "csrc", "tokens.hip")
+SRCS = (SRC, TOKENS_SRC)
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgrz.so")
 ARCH = "gfx950"
@@ -35,16 +38,33 @@ def hipcc():
 
 
 def build(out=LIB, extra=(), verbose=False):
-    """Compile the library to ``out`` (atomically replaced) and return its path."""
+    """Compile the library to ``out`` (atomically replaced) and return its path.
+
+    The sources are compiled side by side, each to an object, and linked."""
     tmp = out + ".tmp"
-    cmd = [hipcc(), *FLAGS, *extra, f"-I{INCLUDE}", SRC, "-o", tmp]
+    objs = [f"{out}.{i}.o" for i in range(len(SRCS))]
+    cmds = [[hipcc(), *[f for f in FLAGS if f != "-shared"], *extra, f"-I{INCLUDE}", "-c", src,
+             "-o", obj] for src, obj in zip(SRCS, objs)]
+    link = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *extra, *objs, "-o", tmp]
     if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stderr}")
-    os.replace(tmp, out)
+        for cmd in (*cmds, link):
+            print(" ".join(cmd), flush=True)
+    try:
+        with concurrent.futures.ThreadPoolExecutor(len(cmds)) as pool:
+            runs = list(pool.map(_run, cmds))
+        for res in (*runs, *([] if any(r.returncode for r in runs) else [_run(link)])):
+            if res.returncode != 0:
+                raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stderr}")
+        os.replace(tmp, out)
+    finally:
+        for obj in objs:
+            if os.path.exists(obj):
+                os.remove(obj)
     return out
+
+
+def _run(cmd):
+    return subprocess.run(cmd, capture_output=True, text=True)
 
 
 if __name__ == "__main__":

@@ -1,0 +1,1178 @@
+// tokens.hip -- HIP kernels and C ABI of the operators addressed by token ids
+// (the two ends of a language model's arena) for AMD Instinct MI355X (gfx950,
+// CDNA4, wave64):
+//   dp_embed_lookup         rows of the embedding table, scaled
+//   dp_embed_grad           its gradient: a stable sort of the token ids, then
+//                           a segmented sum over the sorted rows
+//   dp_token_logprobs       log probability of given tokens, entropy, top list
+//   dp_token_logprobs_grad  its gradient
+//   dp_distill_loss         loss against a teacher's top logits
+//   dp_distill_grad         its gradient (and the loss with it)
+//
+// All are bound by HBM: at most some 15 flops per byte.  No float atomics, so
+// every result bit is the same from run to run.
+
+#include <hip/hip_runtime.h>
+
+#include <limits.h>
+#include <stdint.h>
+
+#include "grz.h"
+
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int64_t kMaxRows = INT32_MAX;  // rows and columns of one call
+// dp_embed_grad: ids, table rows and columns whose launches stay below 2^32
+// threads and 2^16 column blocks.
+constexpr int64_t kGradIds = int64_t{1} << 28, kGradRows = int64_t{1} << 26;
+constexpr int64_t kGradCols = int64_t{65535} * 64;
+constexpr int64_t kRowBatch = int64_t{1} << 21;  // rows of one launch of the row kernels
+
+template <typename T> struct NoDeduce { using type = T; };
+
+// Returns the status of this launch alone (hipLaunchKernel's return value).  A
+// dispatch counts its threads in 32 bits; the entry points' limits and
+// row_batches keep below that.
+template <typename... A>
+int launch(void (*kernel)(A...), dim3 grid, dim3 block, hipStream_t stream,
+           typename NoDeduce<A>::type... a) {
+  if (static_cast<uint64_t>(grid.x) * block.x > UINT32_MAX) return GRZ_ERANGE;
+  void* params[] = {static_cast<void*>(&a)...};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, params, 0,
+                         stream) == hipSuccess ? GRZ_OK : GRZ_EHIP;
+}
+
+constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+bool float_type(int dtype) { return dtype == GRZ_F32 || dtype == GRZ_BF16; }
+size_t elem_size(int dtype) { return dtype == GRZ_F32 ? 4 : 2; }
+
+// A row matrix as the entry points take it: `rows` x `cols` values of `dtype`,
+// row r at data + r * stride elements.
+int check_matrix(const void* data, int dtype, int64_t rows, int64_t cols, int64_t stride) {
+  if (!float_type(dtype) || rows < 0 || cols < 0) return GRZ_EINVAL;
+  if (rows > kMaxRows || cols > kMaxRows) return GRZ_ERANGE;
+  if (stride < cols) return GRZ_EINVAL;
+  if (stride > (INT64_MAX >> 4) / (rows > 0 ? rows : 1)) return GRZ_ERANGE;
+  if (rows == 0 || cols == 0) return GRZ_OK;
+  if (data == nullptr) return GRZ_EINVAL;
+  return aligned(data, elem_size(dtype)) ? GRZ_OK : GRZ_EALIGN;
+}
+
+// Bytes from the first element of a row matrix to behind its last one.
+size_t span_of(int dtype, int64_t rows, int64_t cols, int64_t stride) {
+  if (rows == 0 || cols == 0) return 0;
+  return elem_size(dtype) * static_cast<size_t>((rows - 1) * stride + cols);
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
+int check_ids(const void* ids, int id_bits, int64_t n) {
+  if ((id_bits != 32 && id_bits != 64) || n < 0) return GRZ_EINVAL;
+  if (n > kMaxRows) return GRZ_ERANGE;
+  if (n == 0) return GRZ_OK;
+  if (ids == nullptr) return GRZ_EINVAL;
+  return aligned(ids, id_bits / 8) ? GRZ_OK : GRZ_EALIGN;
+}
+
+// ---------------------------------------------------------------------------
+// Elements.  bf16 values are uint16 patterns; widening is exact, narrowing is
+// round-to-nearest-even with a quiet NaN.
+
+__device__ __forceinline__ float widen(uint16_t v) {
+  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+__device__ __forceinline__ float widen(float v) { return v; }
+
+__device__ __forceinline__ uint32_t bf16_bits(float f) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+}
+__device__ __forceinline__ void put(uint16_t* p, float f) {
+  *p = static_cast<uint16_t>(bf16_bits(f));
+}
+__device__ __forceinline__ void put(float* p, float f) { *p = f; }
+
+// N consecutive elements in one access (8 or 16 bytes; the address is aligned
+// for it), as fp32.
+template <typename T, int N>
+__device__ __forceinline__ void load_vec(const T* p, float (&x)[N]) {
+  if constexpr (N == 1) {
+    x[0] = widen(*p);
+  } else if constexpr (sizeof(T) == 2) {
+    if constexpr (N == 8) {
+      const u32x4 u = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
+    } else {
+      static_assert(N == 4, "bf16 vectors hold 4 or 8 elements");
+      const u32x2 u = *reinterpret_cast<const u32x2*>(p);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < N / 4; ++h) {
+      const u32x4 u = reinterpret_cast<const u32x4*>(p)[h];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[4 * h + i] = __uint_as_float(u[i]);
+    }
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_vec(T* p, const float (&x)[N]) {
+  if constexpr (N == 1) {
+    put(p, x[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    uint32_t u[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      u[i] = bf16_bits(x[2 * i]) | (bf16_bits(x[2 * i + 1]) << 16);
+    if constexpr (N == 8) {
+      *reinterpret_cast<u32x4*>(p) = u32x4{u[0], u[1], u[2], u[3]};
+    } else {
+      static_assert(N == 4, "bf16 vectors hold 4 or 8 elements");
+      *reinterpret_cast<u32x2*>(p) = u32x2{u[0], u[1]};
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < N / 4; ++h) {
+      u32x4 u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(x[4 * h + i]);
+      reinterpret_cast<u32x4*>(p)[h] = u;
+    }
+  }
+}
+
+__device__ __forceinline__ int64_t id_at(const void* ids, int id_bits, int64_t i) {
+  return id_bits == 64 ? static_cast<const int64_t*>(ids)[i]
+                       : static_cast<int64_t>(static_cast<const int32_t*>(ids)[i]);
+}
+
+// ---------------------------------------------------------------------------
+// Lookup: one wave per row, its lanes along the columns.
+
+template <typename TI, typename TO, int VEC>
+__global__ __launch_bounds__(256) void lookup_kernel(const TI* __restrict__ table, int64_t tstride,
+                                                     int64_t vocab, int64_t dim,
+                                                     const void* __restrict__ ids, int id_bits,
+                                                     int64_t row0, int64_t n, float scale,
+                                                     TO* __restrict__ out, int64_t ostride) {
+  const int64_t row = row0 + static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (row >= n) return;
+  const int64_t id = id_at(ids, id_bits, row);
+  const bool ok = id >= 0 && id < vocab;
+  const TI* src = table + (ok ? id : 0) * tstride;
+  TO* dst = out + row * ostride;
+  for (int64_t c = (threadIdx.x & 63) * VEC; c < dim; c += 64 * VEC) {
+    float x[VEC];
+    if (ok) {
+      load_vec<TI, VEC>(src + c, x);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) x[i] *= scale;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) x[i] = 0.0f;
+    }
+    store_vec<TO, VEC>(dst + c, x);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The sort of the token ids: least significant digit first, stable, so that
+// equal ids end up in the order of their positions.  Ids outside [0, vocab)
+// get the key `vocab` and sort behind every row.
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSortItems = 4;
+constexpr int kSortTile = kSortThreads * kSortItems;
+constexpr int kMaxDigitBits = 9;
+constexpr int kDigits = 1 << kMaxDigitBits;
+
+struct SortSrc {
+  const void* ids;  // first pass: the tokens; later passes: null
+  int id_bits;
+  const u32x2* pairs;  // later passes: (key, position)
+  uint32_t vocab;
+};
+
+__device__ __forceinline__ u32x2 sort_pair(const SortSrc& s, int64_t i) {
+  if (s.ids == nullptr) return s.pairs[i];
+  const int64_t id = id_at(s.ids, s.id_bits, i);
+  const uint32_t key = id >= 0 && id < static_cast<int64_t>(s.vocab) ? static_cast<uint32_t>(id)
+                                                                     : s.vocab;
+  return u32x2{key, static_cast<uint32_t>(i)};
+}
+
+// counts[tile][digit] of one tile per workgroup.
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortSrc src, int64_t n,
+                                                                  int shift, int bits,
+                                                                  uint32_t* __restrict__ counts) {
+  __shared__ uint32_t hist[kDigits];
+  const int digits = 1 << bits;
+  for (int d = threadIdx.x; d < digits; d += kSortThreads) hist[d] = 0;
+  __syncthreads();
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kSortTile;
+  for (int j = 0; j < kSortItems; ++j) {
+    const int64_t i = base + j * kSortThreads + threadIdx.x;
+    if (i < n) atomicAdd(&hist[(sort_pair(src, i)[0] >> shift) & (digits - 1)], 1u);
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < digits; d += kSortThreads)
+    counts[static_cast<int64_t>(blockIdx.x) * digits + d] = hist[d];
+}
+
+// One pass: every pair of the tile goes to its place among all n.  Wave w of
+// the workgroup holds 64 * kSortItems consecutive pairs, 64 at a time; a
+// pair's rank among the equal digits before it in its wave comes from the
+// lanes' ballots of each digit bit.
+__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
+    SortSrc src, int64_t n, int shift, int bits, const uint32_t* __restrict__ counts,
+    u32x2* __restrict__ out) {
+  __shared__ uint32_t first[kDigits];                // where the tile's run of a digit begins
+  __shared__ uint16_t wave_count[kSortWaves][kDigits];  // then each wave's first rank in the tile
+  __shared__ uint32_t wave_sum[kSortWaves];
+  const int digits = 1 << bits;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t tiles = ceil_div(n, kSortTile);
+  for (int w = 0; w < kSortWaves; ++w)
+    for (int d = tid; d < digits; d += kSortThreads) wave_count[w][d] = 0;
+  // Pairs of a digit in earlier tiles and in all; then the exclusive scan over the digits.
+  uint32_t before = 0, total = 0;
+  if (tid < digits) {
+    for (int64_t t = 0; t < tiles; ++t) {
+      const uint32_t c = counts[t * digits + tid];
+      before += t < blockIdx.x ? c : 0u;
+      total += c;
+    }
+  }
+  uint32_t scan = total;
+  for (int s = 1; s < 64; s <<= 1) {
+    const uint32_t o = __shfl_up(scan, s, 64);
+    scan += lane >= s ? o : 0u;
+  }
+  if (lane == 63) wave_sum[wave] = scan;
+  __syncthreads();
+  uint32_t wbase = 0;
+  for (int w = 0; w < wave; ++w) wbase += wave_sum[w];
+  if (tid < digits) first[tid] = wbase + scan - total + before;
+
+  u32x2 pair[kSortItems];
+  uint32_t rank[kSortItems];
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kSortTile + wave * 64 * kSortItems;
+#pragma unroll
+  for (int j = 0; j < kSortItems; ++j) {
+    const int64_t i = base + j * 64 + lane;
+    if (i < n) pair[j] = sort_pair(src, i);
+  }
+#pragma unroll
+  for (int j = 0; j < kSortItems; ++j) {
+    const bool in = base + j * 64 + lane < n;
+    const uint32_t d = in ? (pair[j][0] >> shift) & (digits - 1) : 0u;
+    uint64_t same = __ballot(in);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t v = __ballot((d >> b) & 1u);
+      same &= ((d >> b) & 1u) ? v : ~v;
+    }
+    const uint32_t earlier = static_cast<uint32_t>(__popcll(same & ((1ull << lane) - 1)));
+    uint32_t r = 0;
+    if (in) r = wave_count[wave][d];
+    if (in && earlier == 0)
+      wave_count[wave][d] = static_cast<uint16_t>(r + static_cast<uint32_t>(__popcll(same)));
+    rank[j] = r + earlier;
+  }
+  __syncthreads();
+  for (int d = tid; d < digits; d += kSortThreads) {
+    uint32_t sum = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = wave_count[w][d];
+      wave_count[w][d] = static_cast<uint16_t>(sum);
+      sum += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kSortItems; ++j) {
+    if (base + j * 64 + lane < n) {
+      const uint32_t d = (pair[j][0] >> shift) & (digits - 1);
+      out[first[d] + wave_count[wave][d] + rank[j]] = pair[j];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The gradient over the sorted pairs.  The pairs are cut into chunks of equal
+// size; a wave sums one chunk's rows over its columns, run of equal keys by
+// run.  A run inside the chunk is written to its row; one that began in an
+// earlier chunk or goes on in the next leaves its sum in `partial`
+// (chunk, 0: began earlier; 1: begins here and goes on), which join_kernel
+// adds up in chunk order.
+
+constexpr int kChunk = 32;
+
+template <typename TO>
+__device__ __forceinline__ float old_of(const TO* p) { return widen(*p); }
+
+template <typename TO, int VEC>
+__device__ __forceinline__ void finish_row(TO* dst, float (&acc)[VEC], float scale,
+                                           int accumulate) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] *= scale;
+  if (accumulate) {
+    float old[VEC];
+    load_vec<TO, VEC>(dst, old);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] += old[i];
+  }
+  store_vec<TO, VEC>(dst, acc);
+}
+
+template <typename TO, int VEC>
+__global__ __launch_bounds__(256) void zero_rows_kernel(TO* __restrict__ dst, int64_t stride,
+                                                        int64_t rows, int64_t dim) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  float zero[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) zero[i] = 0.0f;
+  for (int64_t c = (threadIdx.x & 63) * VEC; c < dim; c += 64 * VEC)
+    store_vec<TO, VEC>(dst + row * stride + c, zero);
+}
+
+template <typename TI, typename TO, int VEC>
+__global__ __launch_bounds__(64) void embed_grad_kernel(
+    const TI* __restrict__ dout, int64_t istride, const u32x2* __restrict__ pairs, int64_t n,
+    uint32_t vocab, int64_t dim, float scale, int accumulate, float* __restrict__ partial,
+    TO* __restrict__ dtable, int64_t ostride) {
+  const int lane = threadIdx.x;
+  const int64_t chunk = blockIdx.x;
+  const int64_t base = chunk * kChunk;
+  const int cnt = static_cast<int>(n - base < kChunk ? n - base : kChunk);
+  u32x2 mine = {vocab, 0};
+  if (lane < cnt) mine = pairs[base + lane];
+  const uint32_t prev = base > 0 ? pairs[base - 1][0] : vocab;
+  const uint32_t next = base + cnt < n ? pairs[base + cnt][0] : vocab;
+  const int64_t col = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * VEC;
+  const bool on = col < dim;
+  float acc[VEC];
+  bool begun = false;  // the current run began in this chunk
+  for (int e = 0; e < cnt; ++e) {
+    const uint32_t key = __builtin_amdgcn_readlane(mine[0], e);
+    if (key == vocab) break;  // nothing but ids of no row from here on
+    const uint32_t pos = __builtin_amdgcn_readlane(mine[1], e);
+    const uint32_t left = e > 0 ? __builtin_amdgcn_readlane(mine[0], e - 1) : prev;
+    const uint32_t right = e + 1 < cnt ? __builtin_amdgcn_readlane(mine[0], e + 1) : next;
+    float x[VEC];
+    if (on) load_vec<TI, VEC>(dout + static_cast<int64_t>(pos) * istride + col, x);
+    if (key != left || e == 0) {
+      begun = key != left;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] = x[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] += x[i];
+    }
+    if (!on) continue;
+    if (!begun && (key != right || e + 1 == cnt)) {
+      store_vec<float, VEC>(partial + (chunk * 2) * dim + col, acc);
+    } else if (key != right) {
+      finish_row<TO, VEC>(dtable + static_cast<int64_t>(key) * ostride + col, acc, scale,
+                          accumulate);
+    } else if (e + 1 == cnt) {
+      store_vec<float, VEC>(partial + (chunk * 2 + 1) * dim + col, acc);
+    }
+  }
+}
+
+// One workgroup per (chunk border, column block); the border where a run first
+// crosses adds the whole run: its four waves take a quarter of the run's
+// partial sums each, in order, then the four in order.
+template <typename TO, int VEC>
+__global__ __launch_bounds__(256) void join_kernel(const u32x2* __restrict__ pairs, int64_t n,
+                                                   uint32_t vocab, int64_t dim, float scale,
+                                                   int accumulate,
+                                                   const float* __restrict__ partial,
+                                                   TO* __restrict__ dtable, int64_t ostride) {
+  __shared__ float part[4][64 * VEC];
+  const int64_t c = static_cast<int64_t>(blockIdx.x) + 1;  // border between chunks c - 1 and c
+  const uint32_t key = pairs[c * kChunk][0];
+  if (key == vocab || pairs[c * kChunk - 1][0] != key) return;
+  if (c > 1 && pairs[(c - 1) * kChunk - 1][0] == key) return;  // crossed an earlier border
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // The last chunk that begins with the key: 64 probes at a time.
+  const int64_t chunks = ceil_div(n, kChunk);
+  int64_t lo = c, hi = chunks;
+  while (hi - lo > 1) {
+    const int64_t step = ceil_div(hi - lo, 64);
+    const int64_t at = lo + lane * step;
+    const bool same = at < hi && pairs[at * kChunk][0] == key;
+    lo += (__popcll(__ballot(same)) - 1) * step;
+    hi = lo + step < hi ? lo + step : hi;
+  }
+  const int64_t count = lo - c + 2;  // chunks c - 1 .. lo
+  const int64_t share = ceil_div(count, 4);
+  const int64_t from = wave * share, to = from + share < count ? from + share : count;
+  const int64_t col = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * VEC;
+  const bool on = col < dim;
+  float acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+  if (on) {
+    for (int64_t k = from; k < to; ++k) {
+      float x[VEC];
+      load_vec<float, VEC>(partial + ((c - 1 + k) * 2 + (k == 0 ? 1 : 0)) * dim + col, x);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] += x[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) part[wave][lane * VEC + i] = acc[i];
+  __syncthreads();
+  if (wave == 0 && on) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      acc[i] = ((part[0][lane * VEC + i] + part[1][lane * VEC + i]) +
+                part[2][lane * VEC + i]) + part[3][lane * VEC + i];
+    finish_row<TO, VEC>(dtable + static_cast<int64_t>(key) * ostride + col, acc, scale,
+                        accumulate);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows over the vocabulary.  One workgroup of NT threads per row.  The row is
+// read as 16-byte vectors from its first 16-byte border on; the elements
+// before and behind them (fewer than two vectors) go one to a thread, so that
+// nothing outside the row is touched.
+
+template <typename T, int NT> struct Row {
+  static constexpr int E = 16 / sizeof(T);
+  const T* p;
+  int head, nvec;     // elements before the first vector; vectors
+  int edge;           // this thread's single element, or -1
+
+  __device__ __forceinline__ Row(const T* row, int vocab) : p(row) {
+    const int skip = static_cast<int>((16 - reinterpret_cast<uintptr_t>(row) % 16) % 16 /
+                                      sizeof(T));
+    head = skip < vocab ? skip : vocab;
+    nvec = (vocab - head) / E;
+    const int tail0 = head + nvec * E;
+    const int t = threadIdx.x;
+    edge = t < head ? t : t - head < vocab - tail0 ? tail0 + t - head : -1;
+  }
+  // f(x, index) for each of this thread's elements.
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+    for (int v = threadIdx.x; v < nvec; v += NT) {
+      float x[E];
+      load_vec<T, E>(p + head + v * E, x);
+#pragma unroll
+      for (int i = 0; i < E; ++i) f(x[i], head + v * E + i);
+    }
+    if (edge >= 0) f(widen(p[edge]), edge);
+  }
+  // dst[index] = f(x, index) over the row; dst may be the row itself.
+  template <typename F> __device__ __forceinline__ void map(T* dst, F f) const {
+    const bool vec = reinterpret_cast<uintptr_t>(dst + head) % 16 == 0;
+    for (int v = threadIdx.x; v < nvec; v += NT) {
+      float x[E];
+      load_vec<T, E>(p + head + v * E, x);
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[i] = f(x[i]);
+      if (vec) {
+        store_vec<T, E>(dst + head + v * E, x);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) put(dst + head + v * E + i, x[i]);
+      }
+    }
+    if (edge >= 0) put(dst + edge, f(widen(p[edge])));
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void zero_row(T* dst, int vocab, int nt) {
+  for (int i = threadIdx.x; i < vocab; i += nt) dst[i] = static_cast<T>(0);
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+// exp(d) underflows to zero far above this, so terms of exp(d) * d can be cut
+// here: 0 * -inf (a masked element) becomes 0.
+constexpr float kLowest = -1.0e4f;
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) v = fmaxf(v, __shfl_xor(v, s, 64));
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) v += __shfl_xor(v, s, 64);
+  return v;
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const uint64_t o = __shfl_xor(static_cast<unsigned long long>(v), s, 64);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+template <int NT>
+__device__ __forceinline__ float block_max(float v, float* lds) {
+  v = wave_max(v);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = lds[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) v = fmaxf(v, lds[w]);
+    __syncthreads();
+  }
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ float block_sum(float v, float* lds) {
+  v = wave_sum(v);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = lds[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) v += lds[w];
+    __syncthreads();
+  }
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* lds) {
+  v = wave_max(v);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = lds[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) v = lds[w] > v ? lds[w] : v;
+    __syncthreads();
+  }
+  return v;
+}
+
+// The order of the top list: larger values first, then lower indices, as one
+// unsigned number (larger is earlier).  -0 and +0 are equal; NaN comes before
+// +inf.
+__device__ __forceinline__ uint64_t order_of(float x, int index) {
+  uint32_t u = __float_as_uint(x);
+  if ((u & 0x7fffffffu) > 0x7f800000u) {
+    u = 0xffffffffu;
+  } else if (x == 0.0f) {
+    u = 0x80000000u;
+  } else {
+    u = u & 0x80000000u ? ~u : u | 0x80000000u;
+  }
+  return (static_cast<uint64_t>(u) << 32) | (0xffffffffu - static_cast<uint32_t>(index));
+}
+
+template <typename T> struct LogprobArgs {
+  int64_t row0;  // first row of the launch
+  const T* x;
+  int64_t stride;
+  int vocab;
+  const void* targets;
+  int id_bits;
+  int top;
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  // gradient
+  const float* glogprob;
+  const float* gentropy;
+  T* dx;
+  int64_t dstride;
+};
+
+// m = max x; S = sum exp(x - m); A = sum exp(x - m) (x - m).
+// log p_t = x_t - m - log S; H = log S - A / S.
+template <typename T, int NT, bool GRAD>
+__global__ __launch_bounds__(NT) void logprob_kernel(LogprobArgs<T> a) {
+  __shared__ float lds[NT / 64];
+  __shared__ uint64_t lds64[NT / 64];
+  const int64_t i = a.row0 + blockIdx.x;
+  const int64_t target = a.targets != nullptr ? id_at(a.targets, a.id_bits, i) : -1;
+  const bool given = target >= 0 && target < a.vocab;
+  float glp = 0.0f, gent = 0.0f;
+  bool flat = false;
+  if constexpr (GRAD) {
+    glp = given && a.glogprob != nullptr ? a.glogprob[i] : 0.0f;
+    gent = a.gentropy != nullptr ? a.gentropy[i] : 0.0f;
+    flat = glp == 0.0f && gent == 0.0f;
+    if (flat && a.logprob == nullptr && a.entropy == nullptr) {
+      zero_row(a.dx + i * a.dstride, a.vocab, NT);
+      return;
+    }
+  }
+  const T* row = a.x + i * a.stride;
+  const Row<T, NT> r(row, a.vocab);
+  const float xt = given ? widen(row[target]) : 0.0f;
+  float m = -INFINITY;
+  r.each([&](float x, int) { m = fmaxf(m, x); });
+  m = block_max<NT>(m, lds);
+  float s = 0.0f, ent = 0.0f;
+  r.each([&](float x, int) {
+    const float d = x - m;
+    const float e = __builtin_amdgcn_exp2f(d * kLog2e);
+    s += e;
+    ent = fmaf(e, fmaxf(d, kLowest), ent);
+  });
+  s = block_sum<NT>(s, lds);
+  ent = block_sum<NT>(ent, lds);
+  const float logs = logf(s);
+  const float h = logs - ent / s;
+  if (threadIdx.x == 0) {
+    if (a.logprob != nullptr) a.logprob[i] = given ? xt - m - logs : 0.0f;
+    if (a.entropy != nullptr) a.entropy[i] = h;
+  }
+  if constexpr (GRAD) {
+    T* dx = a.dx + i * a.dstride;
+    if (flat) {
+      __syncthreads();  // in place: the row has been read
+      zero_row(dx, a.vocab, NT);
+      return;
+    }
+    const float base = glp + gent * h;
+    r.map(dx, [&](float x) {
+      const float lq = (x - m) - logs;
+      const float q = __builtin_amdgcn_exp2f(lq * kLog2e);
+      return -q * fmaf(gent, fmaxf(lq, kLowest), base);
+    });
+    if (given) {
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const float lq = (xt - m) - logs;
+        const float q = __builtin_amdgcn_exp2f(lq * kLog2e);
+        put(dx + target, glp - q * fmaf(gent, fmaxf(lq, kLowest), base));
+      }
+    }
+  } else {
+    uint64_t last = ~0ull;
+    for (int k = 0; k < a.top; ++k) {
+      uint64_t best = 0;
+      r.each([&](float x, int index) {
+        const uint64_t o = order_of(x, index);
+        if (o < last && o > best) best = o;
+      });
+      best = block_max<NT>(best, lds64);
+      last = best;
+      if (threadIdx.x == 0) {
+        const uint32_t index = 0xffffffffu - static_cast<uint32_t>(best);
+        a.top_ids[i * a.top + k] = static_cast<int32_t>(index);
+        a.top_logprobs[i * a.top + k] = widen(row[index]) - m - logs;
+      }
+    }
+  }
+}
+
+template <typename T> struct DistillArgs {
+  int64_t row0;  // first row of the launch
+  const T* x;
+  int64_t stride;
+  int vocab;
+  const void* ids;
+  int id_bits;
+  const void* teacher;
+  int teacher_bf16;
+  int k;
+  float inv_tau;
+  float tau;
+  float grad_scale;
+  const float* weights;
+  float* loss;
+  T* dx;
+  int64_t dstride;
+};
+
+// p = softmax over the listed z / tau, q = softmax over the row of x / tau:
+// loss = w tau^2 sum_j p_j (log p_j - log q_j), dx = w c tau (q - p).
+template <typename T, int NT, bool GRAD>
+__global__ __launch_bounds__(NT) void distill_kernel(DistillArgs<T> a) {
+  __shared__ float lds[NT / 64];
+  __shared__ int32_t id[GRZ_MAX_TOP];
+  __shared__ float p[GRZ_MAX_TOP], lp[GRZ_MAX_TOP];
+  __shared__ int listed;
+  const int64_t i = a.row0 + blockIdx.x;
+  const float w = a.weights != nullptr ? a.weights[i] : 1.0f;
+  const T* row = a.x + i * a.stride;
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    float z[GRZ_MAX_TOP / 64];
+    float zm = -INFINITY;
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < GRZ_MAX_TOP / 64; ++j) {
+      const int e = j * 64 + lane;
+      z[j] = -INFINITY;
+      if (e < a.k) {
+        const int64_t at = i * a.k + e;
+        const int64_t v = id_at(a.ids, a.id_bits, at);
+        const bool ok = v >= 0 && v < a.vocab;
+        const float t = a.teacher_bf16 ? widen(static_cast<const uint16_t*>(a.teacher)[at])
+                                       : static_cast<const float*>(a.teacher)[at];
+        if (ok) z[j] = t;
+        any = any || (ok && !(t == -INFINITY));
+        id[e] = ok ? static_cast<int32_t>(v) : -1;
+      }
+      zm = fmaxf(zm, z[j]);
+    }
+    zm = wave_max(zm);
+    float sum = 0.0f, e[GRZ_MAX_TOP / 64];
+#pragma unroll
+    for (int j = 0; j < GRZ_MAX_TOP / 64; ++j) {
+      z[j] = (z[j] - zm) * a.inv_tau;
+      e[j] = j * 64 + lane < a.k ? __builtin_amdgcn_exp2f(z[j] * kLog2e) : 0.0f;
+      sum += e[j];
+    }
+    sum = wave_sum(sum);
+    const float logs = logf(sum), inv = 1.0f / sum;
+#pragma unroll
+    for (int j = 0; j < GRZ_MAX_TOP / 64; ++j) {
+      const int q = j * 64 + lane;
+      if (q < a.k) {
+        p[q] = e[j] * inv;
+        lp[q] = z[j] - logs;
+      }
+    }
+    if (lane == 0) listed = __ballot(any) != 0;
+    else (void)__ballot(any);
+  }
+  __syncthreads();
+  T* dx = nullptr;
+  if constexpr (GRAD) dx = a.dx + i * a.dstride;
+  if (w == 0.0f || !listed) {
+    if (threadIdx.x == 0 && a.loss != nullptr) a.loss[i] = 0.0f;
+    if constexpr (GRAD) zero_row(dx, a.vocab, NT);
+    return;
+  }
+  const Row<T, NT> r(row, a.vocab);
+  float m = -INFINITY;
+  r.each([&](float x, int) { m = fmaxf(m, x); });
+  m = block_max<NT>(m, lds);
+  float s = 0.0f;
+  const float l2 = kLog2e * a.inv_tau;
+  r.each([&](float x, int) { s += __builtin_amdgcn_exp2f((x - m) * l2); });
+  s = block_sum<NT>(s, lds);
+  const float logs = logf(s);
+  // The listed tokens: one thread each of the first GRZ_MAX_TOP.
+  float xj[GRZ_MAX_TOP / 64];
+  if (threadIdx.x < 64) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < GRZ_MAX_TOP / 64; ++j) {
+      const int e = j * 64 + static_cast<int>(threadIdx.x);
+      xj[j] = 0.0f;
+      if (e < a.k && id[e] >= 0) {
+        xj[j] = (widen(row[id[e]]) - m) * a.inv_tau - logs;
+        if (p[e] != 0.0f) sum += p[e] * (lp[e] - xj[j]);
+      }
+    }
+    sum = wave_sum(sum);
+    if (threadIdx.x == 0 && a.loss != nullptr) a.loss[i] = w * a.tau * a.tau * sum;
+  }
+  if constexpr (GRAD) {
+    __syncthreads();  // in place: the listed elements have been read
+    const float c = w * a.grad_scale * a.tau;
+    const float log2s = logs * kLog2e;
+    r.map(dx, [&](float x) { return c * __builtin_amdgcn_exp2f((x - m) * l2 - log2s); });
+    __syncthreads();
+    if (threadIdx.x < 64) {
+#pragma unroll
+      for (int j = 0; j < GRZ_MAX_TOP / 64; ++j) {
+        const int e = j * 64 + static_cast<int>(threadIdx.x);
+        if (e < a.k && id[e] >= 0) {
+          float target = 0.0f;
+          bool first = true;
+          for (int f = 0; f < a.k; ++f) {
+            if (id[f] == id[e]) {
+              target += p[f];
+              first = first && f >= e;
+            }
+          }
+          if (first) put(dx + id[e], c * (__builtin_amdgcn_exp2f(xj[j] * kLog2e) - target));
+        }
+      }
+    }
+  }
+}
+
+// One workgroup per row, kRowBatch rows per launch.
+template <typename T, bool GRAD>
+int logprob_launch(LogprobArgs<T> a, int64_t n, hipStream_t stream) {
+  for (a.row0 = 0; a.row0 < n; a.row0 += kRowBatch) {
+    const int64_t rows = n - a.row0 < kRowBatch ? n - a.row0 : kRowBatch;
+    const int st = launch(logprob_kernel<T, 256, GRAD>, dim3(static_cast<unsigned>(rows)),
+                          dim3(256), stream, a);
+    if (st != GRZ_OK) return st;
+  }
+  return GRZ_OK;
+}
+
+template <typename T, bool GRAD>
+int distill_launch(DistillArgs<T> a, int64_t n, hipStream_t stream) {
+  for (a.row0 = 0; a.row0 < n; a.row0 += kRowBatch) {
+    const int64_t rows = n - a.row0 < kRowBatch ? n - a.row0 : kRowBatch;
+    const int st = launch(distill_kernel<T, 256, GRAD>, dim3(static_cast<unsigned>(rows)),
+                          dim3(256), stream, a);
+    if (st != GRZ_OK) return st;
+  }
+  return GRZ_OK;
+}
+
+// Whether dlogits may be written while logits are read: the same matrix, or
+// apart from it.
+int check_pair(const void* x, int dtype, int64_t n, int64_t vocab, int64_t stride,
+               const void* dx, int64_t dstride) {
+  const int st = check_matrix(dx, dtype, n, vocab, dstride);
+  if (st != GRZ_OK) return st;
+  if (x == dx && stride == dstride) return GRZ_OK;
+  return overlap(x, span_of(dtype, n, vocab, stride), dx, span_of(dtype, n, vocab, dstride))
+             ? GRZ_EINVAL : GRZ_OK;
+}
+
+template <typename T>
+int logprobs_entry(const void* logits, int64_t n, int64_t vocab, int64_t stride,
+                   const void* targets, int id_bits, int top, float* logprob, float* entropy,
+                   int32_t* top_ids, float* top_logprobs, const float* glogprob,
+                   const float* gentropy, void* dlogits, int64_t dstride, hipStream_t stream) {
+  LogprobArgs<T> a{0, static_cast<const T*>(logits), stride, static_cast<int>(vocab), targets,
+                   id_bits, top, logprob, entropy, top_ids, top_logprobs, glogprob, gentropy,
+                   static_cast<T*>(dlogits), dstride};
+  return dlogits != nullptr ? logprob_launch<T, true>(a, n, stream)
+                            : logprob_launch<T, false>(a, n, stream);
+}
+
+int check_list(const float* p) { return p == nullptr || aligned(p, 4) ? GRZ_OK : GRZ_EALIGN; }
+
+template <typename T>
+int distill_run(const void* logits, int64_t n, int64_t vocab, int64_t stride, const void* ids,
+                int id_bits, const void* teacher, int teacher_dtype, int k, float temperature,
+                const float* weights, float grad_scale, float* loss, void* dlogits,
+                int64_t dstride, hipStream_t stream) {
+  DistillArgs<T> a{0, static_cast<const T*>(logits), stride, static_cast<int>(vocab), ids, id_bits,
+                   teacher, teacher_dtype == GRZ_BF16, k, 1.0f / temperature, temperature,
+                   grad_scale, weights, loss, static_cast<T*>(dlogits), dstride};
+  return dlogits != nullptr ? distill_launch<T, true>(a, n, stream)
+                            : distill_launch<T, false>(a, n, stream);
+}
+
+int distill_entry(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t stride,
+                  const void* ids, int id_bits, const void* teacher, int teacher_dtype, int k,
+                  float temperature, const float* weights, float grad_scale, float* loss,
+                  bool grad, void* dlogits, int64_t dstride, hipStream_t stream) {
+  int st = check_matrix(logits, dtype, n, vocab, stride);
+  if (st != GRZ_OK) return st;
+  if (k < 1 || k > GRZ_MAX_TOP || !float_type(teacher_dtype)) return GRZ_EINVAL;
+  if (!(temperature > 0.0f) || !(temperature < INFINITY) || !(1.0f / temperature < INFINITY))
+    return GRZ_EINVAL;
+  if (n > kMaxRows / k) return GRZ_ERANGE;
+  if ((st = check_ids(ids, id_bits, n * k)) != GRZ_OK) return st;
+  if (n == 0) return GRZ_OK;
+  if (vocab < 1 || teacher == nullptr) return GRZ_EINVAL;
+  if (!aligned(teacher, elem_size(teacher_dtype))) return GRZ_EALIGN;
+  if (check_list(weights) != GRZ_OK || check_list(loss) != GRZ_OK) return GRZ_EALIGN;
+  if (grad) {
+    if ((st = check_pair(logits, dtype, n, vocab, stride, dlogits, dstride)) != GRZ_OK) return st;
+  } else if (loss == nullptr) {
+    return GRZ_EINVAL;
+  }
+  return dtype == GRZ_BF16
+             ? distill_run<uint16_t>(logits, n, vocab, stride, ids, id_bits, teacher,
+                                     teacher_dtype, k, temperature, weights, grad_scale, loss,
+                                     dlogits, dstride, stream)
+             : distill_run<float>(logits, n, vocab, stride, ids, id_bits, teacher, teacher_dtype,
+                                  k, temperature, weights, grad_scale, loss, dlogits, dstride,
+                                  stream);
+}
+
+// ---------------------------------------------------------------------------
+// Embedding, host side.
+
+int bits_of(int64_t v) {
+  int b = 1;
+  while (v >> b) ++b;
+  return b;
+}
+
+// Workspace of the gradient: two arrays of pairs, the tiles' digit counts and
+// the chunks' partial sums, each on a 256-byte border.
+struct GradPlan {
+  int passes, bits;
+  int64_t tiles, chunks;
+  size_t pairs_a, pairs_b, counts, partial, total;
+};
+
+size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+GradPlan grad_plan(int64_t n, int64_t vocab, int64_t dim) {
+  GradPlan p{};
+  const int need = bits_of(vocab);  // keys 0 .. vocab
+  p.passes = static_cast<int>(ceil_div(need, kMaxDigitBits));
+  p.bits = static_cast<int>(ceil_div(need, p.passes));
+  p.tiles = ceil_div(n, kSortTile);
+  p.chunks = ceil_div(n, kChunk);
+  p.pairs_a = 0;
+  p.pairs_b = up256(static_cast<size_t>(n) * 8);
+  p.counts = p.pairs_b + up256(static_cast<size_t>(n) * 8);
+  p.partial = p.counts + up256(static_cast<size_t>(p.tiles) * kDigits * 4);
+  p.total = p.partial + static_cast<size_t>(p.chunks) * 2 * static_cast<size_t>(dim) * 4;
+  return p;
+}
+
+// Columns per lane that the matrices allow: 4 (8-byte bf16 and 16-byte fp32
+// accesses) or 1.
+template <typename T>
+bool vec_ok(const void* p, int64_t dim, int64_t stride, int vec) {
+  return dim % vec == 0 && stride % vec == 0 && aligned(p, sizeof(T) * vec < 16 ? sizeof(T) * vec : 16);
+}
+
+template <typename TI, typename TO, int VEC>
+int embed_grad_launch(const TI* dout, int64_t istride, const void* ids, int id_bits, int64_t n,
+                      int64_t vocab, int64_t dim, float scale, int accumulate, char* ws,
+                      TO* dtable, int64_t ostride, hipStream_t stream) {
+  int st = GRZ_OK;
+  if (!accumulate) {
+    st = launch(zero_rows_kernel<TO, VEC>, dim3(static_cast<unsigned>(ceil_div(vocab, 4))),
+                dim3(256), stream, dtable, ostride, vocab, dim);
+    if (st != GRZ_OK) return st;
+  }
+  if (n == 0) return GRZ_OK;
+  const GradPlan p = grad_plan(n, vocab, dim);
+  u32x2* pairs[2] = {reinterpret_cast<u32x2*>(ws + p.pairs_a),
+                     reinterpret_cast<u32x2*>(ws + p.pairs_b)};
+  uint32_t* counts = reinterpret_cast<uint32_t*>(ws + p.counts);
+  float* partial = reinterpret_cast<float*>(ws + p.partial);
+  SortSrc src{ids, id_bits, nullptr, static_cast<uint32_t>(vocab)};
+  const dim3 tiles(static_cast<unsigned>(p.tiles)), threads(kSortThreads);
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.bits;
+    st = launch(sort_count_kernel, tiles, threads, stream, src, n, shift, p.bits, counts);
+    if (st != GRZ_OK) return st;
+    st = launch(sort_scatter_kernel, tiles, threads, stream, src, n, shift, p.bits, counts,
+                pairs[pass & 1]);
+    if (st != GRZ_OK) return st;
+    src = SortSrc{nullptr, 0, pairs[pass & 1], static_cast<uint32_t>(vocab)};
+  }
+  const unsigned slabs = static_cast<unsigned>(ceil_div(dim, 64 * VEC));
+  st = launch(embed_grad_kernel<TI, TO, VEC>, dim3(static_cast<unsigned>(p.chunks), slabs),
+              dim3(64), stream, dout, istride, src.pairs, n, static_cast<uint32_t>(vocab), dim,
+              scale, accumulate, partial, dtable, ostride);
+  if (st != GRZ_OK || p.chunks == 1) return st;
+  return launch(join_kernel<TO, VEC>, dim3(static_cast<unsigned>(p.chunks - 1), slabs), dim3(256),
+                stream, src.pairs, n, static_cast<uint32_t>(vocab), dim, scale, accumulate,
+                partial, dtable, ostride);
+}
+
+template <typename TI, typename TO>
+int embed_grad_run(const void* dout, int64_t istride, const void* ids, int id_bits, int64_t n,
+                   int64_t vocab, int64_t dim, float scale, int accumulate, void* ws,
+                   void* dtable, int64_t ostride, hipStream_t stream) {
+  const TI* x = static_cast<const TI*>(dout);
+  TO* y = static_cast<TO*>(dtable);
+  char* w = static_cast<char*>(ws);
+  if (vec_ok<TI>(x, dim, istride, 4) && vec_ok<TO>(y, dim, ostride, 4))
+    return embed_grad_launch<TI, TO, 4>(x, istride, ids, id_bits, n, vocab, dim, scale,
+                                        accumulate, w, y, ostride, stream);
+  return embed_grad_launch<TI, TO, 1>(x, istride, ids, id_bits, n, vocab, dim, scale, accumulate,
+                                      w, y, ostride, stream);
+}
+
+template <typename TI, typename TO, int VEC>
+int lookup_launch(const TI* table, int64_t tstride, int64_t vocab, int64_t dim, const void* ids,
+                  int id_bits, int64_t n, float scale, TO* out, int64_t ostride,
+                  hipStream_t stream) {
+  constexpr int64_t batch = 4 * kRowBatch;  // four rows per workgroup
+  for (int64_t r = 0; r < n; r += batch) {
+    const int64_t rows = n - r < batch ? n - r : batch;
+    const int st = launch(lookup_kernel<TI, TO, VEC>,
+                          dim3(static_cast<unsigned>(ceil_div(rows, 4))), dim3(256), stream,
+                          table, tstride, vocab, dim, ids, id_bits, r, n, scale, out, ostride);
+    if (st != GRZ_OK) return st;
+  }
+  return GRZ_OK;
+}
+
+template <typename TI, typename TO>
+int lookup_run(const void* table, int64_t tstride, int64_t vocab, int64_t dim, const void* ids,
+               int id_bits, int64_t n, float scale, void* out, int64_t ostride,
+               hipStream_t stream) {
+  const TI* x = static_cast<const TI*>(table);
+  TO* y = static_cast<TO*>(out);
+  if (vec_ok<TI>(x, dim, tstride, 8) && vec_ok<TO>(y, dim, ostride, 8))
+    return lookup_launch<TI, TO, 8>(x, tstride, vocab, dim, ids, id_bits, n, scale, y, ostride,
+                                    stream);
+  if (vec_ok<TI>(x, dim, tstride, 4) && vec_ok<TO>(y, dim, ostride, 4))
+    return lookup_launch<TI, TO, 4>(x, tstride, vocab, dim, ids, id_bits, n, scale, y, ostride,
+                                    stream);
+  return lookup_launch<TI, TO, 1>(x, tstride, vocab, dim, ids, id_bits, n, scale, y, ostride,
+                                  stream);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// C ABI
+
+extern "C" {
+
+int dp_embed_lookup(const void* table, int table_dtype, int64_t vocab, int64_t dim,
+                    int64_t table_stride, const void* ids, int id_bits, int64_t n, float scale,
+                    void* out, int out_dtype, int64_t out_stride, hipStream_t stream) {
+  int st = check_ids(ids, id_bits, n);
+  if (st != GRZ_OK) return st;
+  if ((st = check_matrix(out, out_dtype, n, dim, out_stride)) != GRZ_OK) return st;
+  if (n == 0 || dim == 0) return check_matrix(nullptr, table_dtype, 0, dim, table_stride);
+  if ((st = check_matrix(table, table_dtype, vocab, dim, table_stride)) != GRZ_OK) return st;
+  if (overlap(table, span_of(table_dtype, vocab, dim, table_stride), out,
+              span_of(out_dtype, n, dim, out_stride)))
+    return GRZ_EINVAL;
+  if (table_dtype == GRZ_BF16)
+    return out_dtype == GRZ_BF16
+               ? lookup_run<uint16_t, uint16_t>(table, table_stride, vocab, dim, ids, id_bits, n,
+                                                scale, out, out_stride, stream)
+               : lookup_run<uint16_t, float>(table, table_stride, vocab, dim, ids, id_bits, n,
+                                             scale, out, out_stride, stream);
+  return out_dtype == GRZ_BF16
+             ? lookup_run<float, uint16_t>(table, table_stride, vocab, dim, ids, id_bits, n,
+                                           scale, out, out_stride, stream)
+             : lookup_run<float, float>(table, table_stride, vocab, dim, ids, id_bits, n, scale,
+                                        out, out_stride, stream);
+}
+
+size_t dp_embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim) {
+  if (n <= 0 || vocab <= 0 || dim <= 0 || n > kGradIds || vocab > kGradRows || dim > kGradCols)
+    return 0;
+  return grad_plan(n, vocab, dim).total;
+}
+
+int dp_embed_grad(const void* dout, int dout_dtype, int64_t dout_stride, const void* ids,
+                  int id_bits, int64_t n, int64_t vocab, int64_t dim, float scale, int flags,
+                  void* workspace, void* dtable, int dtable_dtype, int64_t dtable_stride,
+                  hipStream_t stream) {
+  if (flags & ~GRZ_ACCUMULATE) return GRZ_EINVAL;
+  int st = check_ids(ids, id_bits, n);
+  if (st != GRZ_OK) return st;
+  if (n > kGradIds || vocab > kGradRows || dim > kGradCols) return GRZ_ERANGE;
+  if ((st = check_matrix(dout, dout_dtype, n, dim, dout_stride)) != GRZ_OK) return st;
+  if ((st = check_matrix(dtable, dtable_dtype, vocab, dim, dtable_stride)) != GRZ_OK) return st;
+  if (vocab == 0 || dim == 0) return GRZ_OK;
+  const size_t need = dp_embed_grad_workspace(n, vocab, dim);
+  if (need > 0) {
+    if (workspace == nullptr) return GRZ_EINVAL;
+    if (!aligned(workspace, 16)) return GRZ_EALIGN;
+  }
+  const size_t table_bytes = span_of(dtable_dtype, vocab, dim, dtable_stride);
+  if (overlap(dout, span_of(dout_dtype, n, dim, dout_stride), dtable, table_bytes) ||
+      overlap(workspace, need, dtable, table_bytes) ||
+      overlap(workspace, need, dout, span_of(dout_dtype, n, dim, dout_stride)) ||
+      overlap(ids, static_cast<size_t>(n) * (id_bits / 8), dtable, table_bytes))
+    return GRZ_EINVAL;
+  const int acc = flags & GRZ_ACCUMULATE ? 1 : 0;
+  if (dout_dtype == GRZ_BF16)
+    return dtable_dtype == GRZ_BF16
+               ? embed_grad_run<uint16_t, uint16_t>(dout, dout_stride, ids, id_bits, n, vocab,
+                                                    dim, scale, acc, workspace, dtable,
+                                                    dtable_stride, stream)
+               : embed_grad_run<uint16_t, float>(dout, dout_stride, ids, id_bits, n, vocab, dim,
+                                                 scale, acc, workspace, dtable, dtable_stride,
+                                                 stream);
+  return dtable_dtype == GRZ_BF16
+             ? embed_grad_run<float, uint16_t>(dout, dout_stride, ids, id_bits, n, vocab, dim,
+                                               scale, acc, workspace, dtable, dtable_stride,
+                                               stream)
+             : embed_grad_run<float, float>(dout, dout_stride, ids, id_bits, n, vocab, dim, scale,
+                                            acc, workspace, dtable, dtable_stride, stream);
+}
+
+int dp_token_logprobs(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t stride,
+                      const void* targets, int id_bits, int top, float* logprob, float* entropy,
+                      int32_t* top_ids, float* top_logprobs, hipStream_t stream) {
+  int st = check_matrix(logits, dtype, n, vocab, stride);
+  if (st != GRZ_OK) return st;
+  if (top < 0 || top > GRZ_MAX_TOP || top > vocab) return GRZ_EINVAL;
+  if (targets != nullptr && (st = check_ids(targets, id_bits, n)) != GRZ_OK) return st;
+  if (logprob != nullptr && targets == nullptr && n > 0) return GRZ_EINVAL;
+  if (n == 0) return GRZ_OK;
+  if (vocab < 1) return GRZ_EINVAL;
+  if (top > 0 && (top_ids == nullptr || top_logprobs == nullptr)) return GRZ_EINVAL;
+  if (logprob == nullptr && entropy == nullptr && top == 0) return GRZ_EINVAL;
+  if (check_list(logprob) != GRZ_OK || check_list(entropy) != GRZ_OK ||
+      check_list(top_logprobs) != GRZ_OK || (top_ids != nullptr && !aligned(top_ids, 4)))
+    return GRZ_EALIGN;
+  return dtype == GRZ_BF16
+             ? logprobs_entry<uint16_t>(logits, n, vocab, stride, targets, id_bits, top, logprob,
+                                        entropy, top_ids, top_logprobs, nullptr, nullptr, nullptr,
+                                        0, stream)
+             : logprobs_entry<float>(logits, n, vocab, stride, targets, id_bits, top, logprob,
+                                     entropy, top_ids, top_logprobs, nullptr, nullptr, nullptr, 0,
+                                     stream);
+}
+
+int dp_token_logprobs_grad(const void* logits, int dtype, int64_t n, int64_t vocab,
+                           int64_t stride, const void* targets, int id_bits,
+                           const float* glogprob, const float* gentropy, float* logprob,
+                           float* entropy, void* dlogits, int64_t dlogits_stride,
+                           hipStream_t stream) {
+  int st = check_matrix(logits, dtype, n, vocab, stride);
+  if (st != GRZ_OK) return st;
+  if (targets != nullptr && (st = check_ids(targets, id_bits, n)) != GRZ_OK) return st;
+  if (n == 0) return GRZ_OK;
+  if (vocab < 1 || (glogprob == nullptr && gentropy == nullptr)) return GRZ_EINVAL;
+  if (targets == nullptr && (glogprob != nullptr || logprob != nullptr)) return GRZ_EINVAL;
+  if (check_list(logprob) != GRZ_OK || check_list(entropy) != GRZ_OK ||
+      check_list(glogprob) != GRZ_OK || check_list(gentropy) != GRZ_OK)
+    return GRZ_EALIGN;
+  if ((st = check_pair(logits, dtype, n, vocab, stride, dlogits, dlogits_stride)) != GRZ_OK)
+    return st;
+  return dtype == GRZ_BF16
+             ? logprobs_entry<uint16_t>(logits, n, vocab, stride, targets, id_bits, 0, logprob,
+                                        entropy, nullptr, nullptr, glogprob, gentropy, dlogits,
+                                        dlogits_stride, stream)
+             : logprobs_entry<float>(logits, n, vocab, stride, targets, id_bits, 0, logprob,
+                                     entropy, nullptr, nullptr, glogprob, gentropy, dlogits,
+                                     dlogits_stride, stream);
+}
+
+int dp_distill_loss(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t stride,
+                    const void* teacher_ids, int id_bits, const void* teacher_logits,
+                    int teacher_dtype, int k, float temperature, const float* weights,
+                    float* loss, hipStream_t stream) {
+  return distill_entry(logits, dtype, n, vocab, stride, teacher_ids, id_bits, teacher_logits,
+                       teacher_dtype, k, temperature, weights, 1.0f, loss, false, nullptr, 0,
+                       stream);
+}
+
+int dp_distill_grad(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t stride,
+                    const void* teacher_ids, int id_bits, const void* teacher_logits,
+                    int teacher_dtype, int k, float temperature, const float* weights,
+                    float grad_scale, float* loss, void* dlogits, int64_t dlogits_stride,
+                    hipStream_t stream) {
+  return distill_entry(logits, dtype, n, vocab, stride, teacher_ids, id_bits, teacher_logits,
+                       teacher_dtype, k, temperature, weights, grad_scale, loss, true, dlogits,
+                       dlogits_stride, stream);
+}
+
+}  // extern "C"

@@ -14,6 +14,16 @@
  *                            second half of a plain all-reduce)
  *   zero1_fused_step         the four above for one shard in one launch
  *
+ * and the operators addressed by token ids, at the two ends of that arena (the
+ * embedding table and the loss over the vocabulary):
+ *
+ *   dp_embed_lookup          scaled rows of the table in a weight arena
+ *   dp_embed_grad            its gradient, into a gradient arena
+ *   dp_token_logprobs        log probability of given tokens, entropy, top list
+ *   dp_token_logprobs_grad   its gradient
+ *   dp_distill_loss          loss against a teacher's top logits
+ *   dp_distill_grad          its gradient
+ *
  * Sources: "Lab 09 -- Parallelism, simulated" s.1 "Ring all-reduce" (the
  * N = 3 schedule table; "Tips": in reduce-scatter step t rank r sends chunk
  * (r - t) mod N and ends owning chunk (r + 1) mod N) and s.2 (sum, then
@@ -94,7 +104,7 @@ enum { GRZ_F32 = 0, GRZ_BF16 = 1, GRZ_F64 = 2 };
  * GRZ_SUM; zero1_adamw_gather takes GRZ_UNEVEN, GRZ_ARGS_DEVICE and
  * GRZ_MEAN_BF16; the
  * all-gathers take GRZ_UNEVEN; zero1_fused_step GRZ_UNEVEN, GRZ_IN_COMPACT,
- * GRZ_ARGS_DEVICE and GRZ_COOPERATIVE.  Their meaning is in each entry
+ * GRZ_ARGS_DEVICE and GRZ_COOPERATIVE; dp_embed_grad GRZ_ACCUMULATE.  Their meaning is in each entry
  * point's comment. */
 enum {
   GRZ_SUM = 1,        /* keep the sum: skip the division by N            */
@@ -107,11 +117,13 @@ enum {
   GRZ_IN_TILED = 128,   /* with GRZ_IN_COMPACT: one receive buffer, the N ranks'
                            values of each piece side by side               */
   GRZ_MEAN_BF16 = 256,  /* the mean (gradient shard) is held in bf16         */
-  GRZ_COOPERATIVE = 512 /* zero1_fused_step: a cooperative launch            */
+  GRZ_COOPERATIVE = 512, /* zero1_fused_step: a cooperative launch           */
+  GRZ_ACCUMULATE = 1024 /* dp_embed_grad: add to what the table gradient holds */
 };
 
 #define GRZ_MAX_RANKS 16    /* N and the number of replicas per call       */
 #define GRZ_PIECE 4096      /* elements per norm piece                      */
+#define GRZ_MAX_TOP 128     /* longest top list of a row                    */
 
 typedef struct {
   int64_t offset; /* first element of the bucket in the arena */
@@ -541,6 +553,150 @@ int zero1_fused_step_args(const void* const* rank_grads, int nranks, int dtype,
                           double max_norm, uint16_t* const* replicas, int nreplicas,
                           double* piece_sqnorm, void* workspace, double* sqnorm_out,
                           float* clip_scale_out, float* mean_out, hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Operators addressed by token ids ("Distributed training" (noeira), "Four
+ * strategies, one interface": weights and gradients are flat arenas; these
+ * read the embedding table in the one and fill its gradient in the other, and
+ * form the loss whose per-token weights dp_reduce_scatter_weighted averages).
+ *
+ * Shared conventions:
+ *
+ *  - Row matrices.  `rows` x `cols` values of GRZ_F32 or GRZ_BF16, row r at
+ *    data + r * stride elements (stride >= cols), aligned to its element: a
+ *    tensor at any place of an arena.  Rows on 16-byte borders are fastest.
+ *    Elements between cols and stride are neither read nor written.
+ *  - Ids.  int32 (id_bits 32) or int64 (id_bits 64) device arrays.  An id
+ *    outside [0, vocab) names no row (padding, ignored targets).
+ *  - Sizes.  At most 2^31 - 1 rows and columns, further limits at the entry
+ *    points; beyond them GRZ_ERANGE.  Calls with n = 0 do nothing (dp_embed_grad
+ *    still zeroes its table).
+ *  - Arithmetic.  Every sum, maximum and exponential in fp32; each output is
+ *    rounded once to its type (bf16: nearest even).  The same call on the same
+ *    values gives the same bits; the order of a vocabulary row's sums follows
+ *    its place on the 16-byte borders, so another layout may round otherwise.
+ *  - Errors, beside each entry point's own: GRZ_EINVAL for a null pointer, a
+ *    type or flag that is not taken, or outputs that overlap an input;
+ *    GRZ_EALIGN; GRZ_ERANGE.
+ */
+
+/*
+ * out[i] = scale * table[ids[i]], a row of zeros where the id names no row.
+ *
+ * table  device, vocab x dim; out  device, n x dim; any of the two types each.
+ */
+int dp_embed_lookup(const void* table, int table_dtype, int64_t vocab, int64_t dim,
+                    int64_t table_stride, const void* ids, int id_bits, int64_t n, float scale,
+                    void* out, int out_dtype, int64_t out_stride, hipStream_t stream);
+
+/* Bytes of workspace dp_embed_grad needs (0 for n = 0, dim = 0 or sizes it refuses). */
+size_t dp_embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
+
+/*
+ * Gradient of dp_embed_lookup with respect to the table:
+ * dtable[v] = scale * sum over i with ids[i] = v of dout[i], and zeros in the
+ * rows that no id names; with GRZ_ACCUMULATE that sum is added to what the row
+ * holds (the head's gradient of a tied table, an earlier micro-batch), rounded
+ * once, and rows no id names are not touched.
+ *
+ * The ids are sorted by a stable sort and each row's sum runs over its
+ * positions in ascending order, cut at fixed places, so the same ids and dout
+ * give the same bits.  ("A4", "Common Mistakes": stray atomics.)
+ *
+ * dout       device, n x dim; dtable  device, vocab x dim.
+ * workspace  device, dp_embed_grad_workspace(n, vocab, dim) bytes, 16-byte
+ *            aligned; needs no initial value.  Calls that may run at the same
+ *            time need one each.
+ * Errors: GRZ_ERANGE beyond 2^28 ids, 2^26 rows or 2^22 - 64 columns.
+ */
+int dp_embed_grad(const void* dout, int dout_dtype, int64_t dout_stride, const void* ids,
+                  int id_bits, int64_t n, int64_t vocab, int64_t dim, float scale, int flags,
+                  void* workspace, void* dtable, int dtable_dtype, int64_t dtable_stride,
+                  hipStream_t stream);
+
+/*
+ * Log probabilities under q = softmax(logits[i]) over the vocabulary.
+ *
+ * logits        device, n x vocab.
+ * targets       device, n ids, or NULL (then logprob is NULL as well).
+ * logprob       device fp32[n]: log q(targets[i]), 0 where the target names no
+ *               token; or NULL.
+ * entropy       device fp32[n]: -sum q log q (a token of q = 0 adds 0); or NULL.
+ * top           0..min(GRZ_MAX_TOP, vocab): length of the top list.
+ * top_ids       device int32[n * top]: the tokens of the largest logits, larger
+ *               first, equal ones by lower id (NaN counts as largest).
+ * top_logprobs  device fp32[n * top]: their log q.
+ * A logit of -inf is a token of probability 0.  A row that holds a NaN or
+ * +inf, or nothing but -inf, has no softmax: its results are NaN (its top ids
+ * are still in order).
+ * Errors: GRZ_EINVAL also when no output is asked for.
+ */
+int dp_token_logprobs(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t stride,
+                      const void* targets, int id_bits, int top, float* logprob, float* entropy,
+                      int32_t* top_ids, float* top_logprobs, hipStream_t stream);
+
+/*
+ * Gradient of dp_token_logprobs' logprob and entropy:
+ * dlogits[i][v] = glogprob[i] (1[v = targets[i]] - q_v)
+ *                 - gentropy[i] q_v (log q_v + H_i).
+ * (glogprob = -weight: the weighted cross entropy's gradient.)
+ *
+ * glogprob, gentropy  device fp32[n], the incoming gradients; either may be
+ *                     NULL for 0, not both.  glogprob counts as 0 where the
+ *                     target names no token; a row with both 0 gets zeros
+ *                     whatever its logits hold.
+ * logprob, entropy    device fp32[n] or NULL, as from dp_token_logprobs.
+ * dlogits             device, n x vocab of the logits' type; may be the logits
+ *                     themselves (same pointer and stride).
+ */
+int dp_token_logprobs_grad(const void* logits, int dtype, int64_t n, int64_t vocab,
+                           int64_t stride, const void* targets, int id_bits,
+                           const float* glogprob, const float* gentropy, float* logprob,
+                           float* entropy, void* dlogits, int64_t dlogits_stride,
+                           hipStream_t stream);
+
+/*
+ * Distillation from a teacher's top logits.  With p = softmax over the k listed
+ * entries of teacher_logits[i] / T and q = softmax over the vocabulary of
+ * logits[i] / T:
+ *
+ *   loss[i] = weights[i] T^2 sum_j p_j (log p_j - log q(teacher_ids[i][j]))
+ *
+ * (k = 1 with the target's id and T = 1 is the cross entropy.)
+ *
+ * logits          device, n x vocab.
+ * teacher_ids     device, n * k ids, contiguous.  An entry that names no token
+ *                 is left out, as is a teacher logit of -inf; a token listed
+ *                 twice has the sum of its entries' p.
+ * teacher_logits  device, n * k values of teacher_dtype (GRZ_F32 or GRZ_BF16),
+ *                 contiguous; log probabilities will do.
+ * k               1..GRZ_MAX_TOP.
+ * temperature     T > 0, finite (and 1 / T finite).
+ * weights         device fp32[n], or NULL for 1.  A row of weight 0, or with
+ *                 nothing listed, has loss 0 and gradient 0 whatever its
+ *                 logits hold.
+ * loss            device fp32[n].
+ * Errors: GRZ_ERANGE also when n * k exceeds 2^31 - 1.
+ */
+int dp_distill_loss(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t stride,
+                    const void* teacher_ids, int id_bits, const void* teacher_logits,
+                    int teacher_dtype, int k, float temperature, const float* weights,
+                    float* loss, hipStream_t stream);
+
+/*
+ * Gradient of grad_scale * sum of dp_distill_loss's losses:
+ * dlogits[i][v] = grad_scale weights[i] T (q_v - sum of p_j with id v).
+ *
+ * loss     as above, from the same pass over the logits; or NULL.
+ * dlogits  device, n x vocab of the logits' type; may be the logits themselves
+ *          (same pointer and stride).
+ */
+int dp_distill_grad(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t stride,
+                    const void* teacher_ids, int id_bits, const void* teacher_logits,
+                    int teacher_dtype, int k, float temperature, const float* weights,
+                    float grad_scale, float* loss, void* dlogits, int64_t dlogits_stride,
+                    hipStream_t stream);
 
 #ifdef __cplusplus
 }
