@@ -459,12 +459,18 @@ __global__ __launch_bounds__(256) void join_kernel(const u32x2* __restrict__ pai
 // read as 16-byte vectors from its first 16-byte border on; the elements
 // before and behind them (fewer than two vectors) go one to a thread, so that
 // nothing outside the row is touched.
+//
+// NV > 0: the row is read once and kept in registers, up to NV vectors per
+// thread, so that its maximum, its sums and its gradient cost one pass over
+// HBM.  NV = 0, for rows too long for that: each step reads the row again.
 
-template <typename T, int NT> struct Row {
+template <typename T, int NT, int NV> struct Row {
   static constexpr int E = 16 / sizeof(T);
   const T* p;
   int head, nvec;     // elements before the first vector; vectors
   int edge;           // this thread's single element, or -1
+  float edge_x;
+  u32x4 kept[NV > 0 ? NV : 1];
 
   __device__ __forceinline__ Row(const T* row, int vocab) : p(row) {
     const int skip = static_cast<int>((16 - reinterpret_cast<uintptr_t>(row) % 16) % 16 /
@@ -474,55 +480,113 @@ template <typename T, int NT> struct Row {
     const int tail0 = head + nvec * E;
     const int t = threadIdx.x;
     edge = t < head ? t : t - head < vocab - tail0 ? tail0 + t - head : -1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int v = j * NT + t;
+      if (v < nvec) kept[j] = *reinterpret_cast<const u32x4*>(p + head + v * E);
+    }
+    edge_x = edge >= 0 ? widen(p[edge]) : 0.0f;
+  }
+  static __device__ __forceinline__ void unpack(u32x4 u, float (&x)[E]) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]);
+    }
+  }
+  // f(vector's elements, index of the first) for each of this thread's vectors.
+  template <typename F> __device__ __forceinline__ void vectors(F f) const {
+    float x[E];
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int v = j * NT + static_cast<int>(threadIdx.x);
+        if (v < nvec) {
+          unpack(kept[j], x);
+          f(x, head + v * E);
+        }
+      }
+    } else {
+      for (int v = threadIdx.x; v < nvec; v += NT) {
+        unpack(*reinterpret_cast<const u32x4*>(p + head + v * E), x);
+        f(x, head + v * E);
+      }
+    }
   }
   // f(x, index) for each of this thread's elements.
   template <typename F> __device__ __forceinline__ void each(F f) const {
-    for (int v = threadIdx.x; v < nvec; v += NT) {
-      float x[E];
-      load_vec<T, E>(p + head + v * E, x);
+    vectors([&](float (&x)[E], int at) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) f(x[i], head + v * E + i);
-    }
-    if (edge >= 0) f(widen(p[edge]), edge);
+      for (int i = 0; i < E; ++i) f(x[i], at + i);
+    });
+    if (edge >= 0) f(edge_x, edge);
   }
-  // dst[index] = f(x, index) over the row; dst may be the row itself.
+  // dst[index] = f(x) over the row; dst may be the row itself.
   template <typename F> __device__ __forceinline__ void map(T* dst, F f) const {
     const bool vec = reinterpret_cast<uintptr_t>(dst + head) % 16 == 0;
-    for (int v = threadIdx.x; v < nvec; v += NT) {
-      float x[E];
-      load_vec<T, E>(p + head + v * E, x);
+    vectors([&](float (&x)[E], int at) {
 #pragma unroll
       for (int i = 0; i < E; ++i) x[i] = f(x[i]);
       if (vec) {
-        store_vec<T, E>(dst + head + v * E, x);
+        store_vec<T, E>(dst + at, x);
       } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) put(dst + head + v * E + i, x[i]);
+        for (int i = 0; i < E; ++i) put(dst + at + i, x[i]);
       }
-    }
-    if (edge >= 0) put(dst + edge, f(widen(p[edge])));
+    });
+    if (edge >= 0) put(dst + edge, f(edge_x));
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void zero_row(T* dst, int vocab, int nt) {
-  for (int i = threadIdx.x; i < vocab; i += nt) dst[i] = static_cast<T>(0);
+template <typename T, int NT>
+__device__ __forceinline__ void zero_row(T* dst, int vocab) {
+  constexpr int E = 16 / sizeof(T);
+  const int skip = static_cast<int>((16 - reinterpret_cast<uintptr_t>(dst) % 16) % 16 /
+                                    sizeof(T));
+  const int head = skip < vocab ? skip : vocab;
+  const int nvec = (vocab - head) / E;
+  for (int v = threadIdx.x; v < nvec; v += NT)
+    *reinterpret_cast<u32x4*>(dst + head + v * E) = u32x4{0, 0, 0, 0};
+  const int t = threadIdx.x, tail0 = head + nvec * E;
+  if (t < head) dst[t] = static_cast<T>(0);
+  else if (t - head < vocab - tail0) dst[tail0 + t - head] = static_cast<T>(0);
 }
 
 constexpr float kLog2e = 1.44269504088896340736f;
-// exp(d) underflows to zero far above this, so terms of exp(d) * d can be cut
-// here: 0 * -inf (a masked element) becomes 0.
+constexpr float kLn2 = 0.69314718055994530942f;
+// 2^d underflows to zero far above this, so terms of 2^d * d can be cut here:
+// 0 * -inf (a masked element) becomes 0.
 constexpr float kLowest = -1.0e4f;
 
+// Reductions.  A wave's in a fixed tree: four steps of lane exchanges inside
+// each row of 16 lanes, then the four rows.
+template <int CTRL> __device__ __forceinline__ float lane_swap(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, 0xf, 0xf,
+                                                     false));
+}
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+
+__device__ __forceinline__ float lane_of(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) v = fmaxf(v, __shfl_xor(v, s, 64));
-  return v;
+  v = fmaxf(v, lane_swap<kSwap1>(v));
+  v = fmaxf(v, lane_swap<kSwap2>(v));
+  v = fmaxf(v, lane_swap<kHalfMirror>(v));
+  v = fmaxf(v, lane_swap<kMirror>(v));
+  return fmaxf(fmaxf(lane_of(v, 0), lane_of(v, 16)), fmaxf(lane_of(v, 32), lane_of(v, 48)));
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) v += __shfl_xor(v, s, 64);
-  return v;
+  v += lane_swap<kSwap1>(v);
+  v += lane_swap<kSwap2>(v);
+  v += lane_swap<kHalfMirror>(v);
+  v += lane_swap<kMirror>(v);
+  return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
 #pragma unroll
@@ -533,59 +597,194 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
   return v;
 }
 
-template <int NT>
-__device__ __forceinline__ float block_max(float v, float* lds) {
+// The whole workgroup's, every thread with the result (every wave reads the
+// waves' values into its lanes and repeats the exchanges).  Each call of a kernel
+// has an LDS array of its own, so one barrier is enough.
+template <int NT> __device__ __forceinline__ float block_max(float v, float* lds) {
   v = wave_max(v);
   if constexpr (NT > 64) {
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = lds[0];
-#pragma unroll
-    for (int w = 1; w < NT / 64; ++w) v = fmaxf(v, lds[w]);
-    __syncthreads();
+    v = lds[threadIdx.x % (NT / 64)];
+    v = fmaxf(v, lane_swap<kSwap1>(v));
+    if constexpr (NT >= 256) v = fmaxf(v, lane_swap<kSwap2>(v));
+    if constexpr (NT >= 512) v = fmaxf(v, lane_swap<kHalfMirror>(v));
+    if constexpr (NT >= 1024) v = fmaxf(v, lane_swap<kMirror>(v));
   }
   return v;
 }
-template <int NT>
-__device__ __forceinline__ float block_sum(float v, float* lds) {
-  v = wave_sum(v);
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = lds[0];
+template <int NT, int M>
+__device__ __forceinline__ void block_sum(float (&v)[M], float (*lds)[M]) {
 #pragma unroll
-    for (int w = 1; w < NT / 64; ++w) v += lds[w];
+  for (int i = 0; i < M; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < M; ++i) lds[threadIdx.x >> 6][i] = v[i];
+    }
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      v[i] = lds[threadIdx.x % (NT / 64)][i];
+      v[i] += lane_swap<kSwap1>(v[i]);
+      if constexpr (NT >= 256) v[i] += lane_swap<kSwap2>(v[i]);
+      if constexpr (NT >= 512) v[i] += lane_swap<kHalfMirror>(v[i]);
+      if constexpr (NT >= 1024) v[i] += lane_swap<kMirror>(v[i]);
+    }
   }
-  return v;
 }
 template <int NT>
 __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* lds) {
   v = wave_max(v);
   if constexpr (NT > 64) {
+    __syncthreads();  // called in a loop on one array
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
     v = lds[0];
 #pragma unroll
     for (int w = 1; w < NT / 64; ++w) v = lds[w] > v ? lds[w] : v;
-    __syncthreads();
   }
   return v;
+}
+
+// Waves per SIMD the kernels are built for: two workgroups of 1024 threads on a
+// CU, so that one's loads and stores run beside the other's arithmetic; with
+// 16 vectors kept the registers hold one.
+constexpr int kept_waves(int nv) { return nv > 8 ? 4 : 8; }
+
+// The row's exponents, in powers of two: an element's is x * l2 - at, l2 =
+// log2(e) / T, with one fused rounding.  `at` = max * l2, rounded, cancels from
+// everything normalised by the sum.  Where max * l2 could overflow (logits at
+// the type's lowest value) the difference is formed first.
+struct Exponent {
+  float inv_tau, l2, max, at;
+  bool plain;
+  __device__ __forceinline__ Exponent(float m, float inv)
+      : inv_tau(inv), l2(kLog2e * inv), max(m), at(m * l2), plain(fabsf(at) < 1.0e30f) {}
+  __device__ __forceinline__ float far(float x) const { return (x - max) * l2; }
+  __device__ __forceinline__ float near(float x) const { return fmaf(x, l2, -at); }
+  __device__ __forceinline__ float of(float x) const { return plain ? near(x) : far(x); }
+  // log q, finite wherever it can be: log2s counts from `at`, not from max * l2.
+  __device__ __forceinline__ float log_q(float x, float log2s) const {
+    return (x - max) * inv_tau - (log2s - of(max)) * kLn2;
+  }
+};
+
+// each() and map() with the exponent's form chosen once for the row.
+template <typename R, typename F>
+__device__ __forceinline__ void each_exponent(const R& r, const Exponent& e, F f) {
+  if (e.plain) r.each([&](float x, int) { f(e.near(x)); });
+  else r.each([&](float x, int) { f(e.far(x)); });
+}
+template <typename R, typename T, typename F>
+__device__ __forceinline__ void map_exponent(const R& r, T* dst, const Exponent& e, F f) {
+  if (e.plain) r.map(dst, [&](float x) { return f(e.near(x)); });
+  else r.map(dst, [&](float x) { return f(e.far(x)); });
 }
 
 // The order of the top list: larger values first, then lower indices, as one
 // unsigned number (larger is earlier).  -0 and +0 are equal; NaN comes before
 // +inf.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t u = __float_as_uint(x);
+  if ((u & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
+  if (x == 0.0f) return 0x80000000u;
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
 __device__ __forceinline__ uint64_t order_of(float x, int index) {
-  uint32_t u = __float_as_uint(x);
-  if ((u & 0x7fffffffu) > 0x7f800000u) {
-    u = 0xffffffffu;
-  } else if (x == 0.0f) {
-    u = 0x80000000u;
-  } else {
-    u = u & 0x80000000u ? ~u : u | 0x80000000u;
+  return (static_cast<uint64_t>(key_of(x)) << 32) | (0xffffffffu - static_cast<uint32_t>(index));
+}
+__device__ __forceinline__ int index_of(uint64_t order) {
+  return static_cast<int>(0xffffffffu - static_cast<uint32_t>(order));
+}
+// The value of a key that is none of NaN's, at least -inf.
+__device__ __forceinline__ float value_of(uint32_t key) {
+  if (key < 0x007fffffu) return -INFINITY;
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+constexpr int kCandidates = 512;
+constexpr int kGroups = 256;
+
+template <int NT> struct TopLds {
+  static constexpr int G = NT < kGroups ? NT : kGroups;
+  uint32_t group[G];
+  uint64_t found[kCandidates];
+  uint32_t bound;
+  uint32_t count;
+  uint64_t best[NT / 64];
+};
+
+// The `top` elements that come first, handed to emit(place, order).
+//
+// The largest elements of G groups of threads (a thread, or a few neighbours)
+// are found first: the top-th largest of those bounds the list from below, and
+// few elements lie at or above it.  They are gathered and each finds its place
+// by counting the ones before it.  The bound is searched over the keys' upper
+// 16 bits.  A row with more candidates than fit (many equal values), or with
+// NaN, takes one search over the row per place instead.
+//
+// own_max: the largest of the thread's elements; exact: the row holds no NaN.
+template <typename T, int NT, int NV, typename F>
+__device__ __forceinline__ void top_of(const Row<T, NT, NV>& r, int vocab, float own_max,
+                                       bool exact, int top, TopLds<NT>& lds, F emit) {
+  constexpr int G = TopLds<NT>::G;
+  const int lane = threadIdx.x & 63;
+  if (exact && top <= G) {
+    float g = own_max;
+    if constexpr (NT / G >= 2) g = fmaxf(g, lane_swap<kSwap1>(g));
+    if constexpr (NT / G >= 4) g = fmaxf(g, lane_swap<kSwap2>(g));
+    static_assert(NT / G <= 4, "groups of up to four lanes");
+    if (threadIdx.x % (NT / G) == 0) lds.group[threadIdx.x / (NT / G)] = key_of(g);
+    if (threadIdx.x == 0) lds.count = 0;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      uint32_t k[G / 64];
+#pragma unroll
+      for (int i = 0; i < G / 64; ++i) k[i] = lds.group[i * 64 + lane];
+      uint32_t bound = 0;
+      for (int b = 31; b >= 16; --b) {
+        const uint32_t c = bound | (1u << b);
+        int have = 0;
+#pragma unroll
+        for (int i = 0; i < G / 64; ++i) have += __popcll(__ballot(k[i] >= c));
+        if (have >= top) bound = c;
+      }
+      if (lane == 0) lds.bound = bound;
+    }
+    __syncthreads();
+    const float bound = value_of(lds.bound);
+    if (own_max >= bound) {
+      r.each([&](float x, int index) {
+        if (x >= bound) {
+          const uint32_t at = atomicAdd(&lds.count, 1u);
+          if (at < kCandidates) lds.found[at] = order_of(x, index);
+        }
+      });
+    }
+    __syncthreads();
+    const int count = static_cast<int>(lds.count);
+    if (count <= kCandidates) {
+      for (int c = threadIdx.x; c < count; c += NT) {
+        const uint64_t mine = lds.found[c];
+        int place = 0;
+        for (int o = 0; o < count; ++o) place += lds.found[o] > mine ? 1 : 0;
+        if (place < top) emit(place, mine);
+      }
+      return;
+    }
   }
-  return (static_cast<uint64_t>(u) << 32) | (0xffffffffu - static_cast<uint32_t>(index));
+  const Row<T, NT, 0> again(r.p, vocab);
+  uint64_t last = ~0ull;
+  for (int k = 0; k < top; ++k) {
+    uint64_t best = 0;
+    again.each([&](float x, int index) {
+      const uint64_t o = order_of(x, index);
+      if (o < last && o > best) best = o;
+    });
+    last = block_max<NT>(best, lds.best);
+    if (threadIdx.x == 0) emit(k, last);
+  }
 }
 
 template <typename T> struct LogprobArgs {
@@ -607,12 +806,12 @@ template <typename T> struct LogprobArgs {
   int64_t dstride;
 };
 
-// m = max x; S = sum exp(x - m); A = sum exp(x - m) (x - m).
-// log p_t = x_t - m - log S; H = log S - A / S.
-template <typename T, int NT, bool GRAD>
-__global__ __launch_bounds__(NT) void logprob_kernel(LogprobArgs<T> a) {
-  __shared__ float lds[NT / 64];
-  __shared__ uint64_t lds64[NT / 64];
+// With d the elements' exponents, S = sum 2^d and A = sum 2^d d:
+// log2 q = d - log2 S, H = (log2 S - A / S) ln 2.
+template <typename T, int NT, int NV, bool GRAD>
+__global__ __launch_bounds__(NT, kept_waves(NV)) void logprob_kernel(LogprobArgs<T> a) {
+  __shared__ float lds_max[NT / 64];
+  __shared__ float lds_sum[NT / 64][2];
   const int64_t i = a.row0 + blockIdx.x;
   const int64_t target = a.targets != nullptr ? id_at(a.targets, a.id_bits, i) : -1;
   const bool given = target >= 0 && target < a.vocab;
@@ -623,68 +822,53 @@ __global__ __launch_bounds__(NT) void logprob_kernel(LogprobArgs<T> a) {
     gent = a.gentropy != nullptr ? a.gentropy[i] : 0.0f;
     flat = glp == 0.0f && gent == 0.0f;
     if (flat && a.logprob == nullptr && a.entropy == nullptr) {
-      zero_row(a.dx + i * a.dstride, a.vocab, NT);
+      zero_row<T, NT>(a.dx + i * a.dstride, a.vocab);
       return;
     }
   }
   const T* row = a.x + i * a.stride;
-  const Row<T, NT> r(row, a.vocab);
+  const Row<T, NT, NV> r(row, a.vocab);
   const float xt = given ? widen(row[target]) : 0.0f;
-  float m = -INFINITY;
-  r.each([&](float x, int) { m = fmaxf(m, x); });
-  m = block_max<NT>(m, lds);
-  float s = 0.0f, ent = 0.0f;
-  r.each([&](float x, int) {
-    const float d = x - m;
-    const float e = __builtin_amdgcn_exp2f(d * kLog2e);
-    s += e;
-    ent = fmaf(e, fmaxf(d, kLowest), ent);
+  float own_max = -INFINITY;
+  r.each([&](float x, int) { own_max = fmaxf(own_max, x); });
+  const Exponent e(block_max<NT>(own_max, lds_max), 1.0f);
+  float sum[2] = {0.0f, 0.0f};
+  each_exponent(r, e, [&](float d) {
+    const float p = __builtin_amdgcn_exp2f(d);
+    sum[0] += p;
+    sum[1] = fmaf(p, fmaxf(d, kLowest), sum[1]);
   });
-  s = block_sum<NT>(s, lds);
-  ent = block_sum<NT>(ent, lds);
-  const float logs = logf(s);
-  const float h = logs - ent / s;
+  block_sum<NT, 2>(sum, lds_sum);
+  const float log2s = log2f(sum[0]);
+  const float h = (log2s - sum[1] / sum[0]) * kLn2;
   if (threadIdx.x == 0) {
-    if (a.logprob != nullptr) a.logprob[i] = given ? xt - m - logs : 0.0f;
+    if (a.logprob != nullptr) a.logprob[i] = given ? e.log_q(xt, log2s) : 0.0f;
     if (a.entropy != nullptr) a.entropy[i] = h;
   }
   if constexpr (GRAD) {
     T* dx = a.dx + i * a.dstride;
     if (flat) {
-      __syncthreads();  // in place: the row has been read
-      zero_row(dx, a.vocab, NT);
+      zero_row<T, NT>(dx, a.vocab);
       return;
     }
-    const float base = glp + gent * h;
-    r.map(dx, [&](float x) {
-      const float lq = (x - m) - logs;
-      const float q = __builtin_amdgcn_exp2f(lq * kLog2e);
-      return -q * fmaf(gent, fmaxf(lq, kLowest), base);
-    });
+    // -q (glp + gent (log q + H)), with log q in powers of two.
+    const float base = glp + gent * h, slope = gent * kLn2;
+    auto value = [&](float d) {
+      const float lq = d - log2s;
+      return -__builtin_amdgcn_exp2f(lq) * fmaf(slope, fmaxf(lq, kLowest), base);
+    };
+    map_exponent(r, dx, e, value);
     if (given) {
       __syncthreads();
-      if (threadIdx.x == 0) {
-        const float lq = (xt - m) - logs;
-        const float q = __builtin_amdgcn_exp2f(lq * kLog2e);
-        put(dx + target, glp - q * fmaf(gent, fmaxf(lq, kLowest), base));
-      }
+      if (threadIdx.x == 0) put(dx + target, glp + value(e.of(xt)));
     }
-  } else {
-    uint64_t last = ~0ull;
-    for (int k = 0; k < a.top; ++k) {
-      uint64_t best = 0;
-      r.each([&](float x, int index) {
-        const uint64_t o = order_of(x, index);
-        if (o < last && o > best) best = o;
-      });
-      best = block_max<NT>(best, lds64);
-      last = best;
-      if (threadIdx.x == 0) {
-        const uint32_t index = 0xffffffffu - static_cast<uint32_t>(best);
-        a.top_ids[i * a.top + k] = static_cast<int32_t>(index);
-        a.top_logprobs[i * a.top + k] = widen(row[index]) - m - logs;
-      }
-    }
+  } else if (a.top > 0) {
+    __shared__ TopLds<NT> lds_top;
+    top_of(r, a.vocab, own_max, sum[0] == sum[0], a.top, lds_top, [&](int place, uint64_t order) {
+      const int index = index_of(order);
+      a.top_ids[i * a.top + place] = index;
+      a.top_logprobs[i * a.top + place] = e.log_q(widen(row[index]), log2s);
+    });
   }
 }
 
@@ -698,6 +882,7 @@ template <typename T> struct DistillArgs {
   const void* teacher;
   int teacher_bf16;
   int k;
+  int top;  // 0: the list's length does not choose the shape
   float inv_tau;
   float tau;
   float grad_scale;
@@ -709,110 +894,115 @@ template <typename T> struct DistillArgs {
 
 // p = softmax over the listed z / tau, q = softmax over the row of x / tau:
 // loss = w tau^2 sum_j p_j (log p_j - log q_j), dx = w c tau (q - p).
-template <typename T, int NT, bool GRAD>
-__global__ __launch_bounds__(NT) void distill_kernel(DistillArgs<T> a) {
-  __shared__ float lds[NT / 64];
+// The first wave holds the list, two entries per lane.
+template <typename T, int NT, int NV, bool GRAD>
+__global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs<T> a) {
+  constexpr int M = GRZ_MAX_TOP / 64;
+  __shared__ float lds_max[NT / 64];
+  __shared__ float lds_sum[NT / 64][1];
   __shared__ int32_t id[GRZ_MAX_TOP];
-  __shared__ float p[GRZ_MAX_TOP], lp[GRZ_MAX_TOP];
+  __shared__ float p[GRZ_MAX_TOP];
   __shared__ int listed;
   const int64_t i = a.row0 + blockIdx.x;
   const float w = a.weights != nullptr ? a.weights[i] : 1.0f;
   const T* row = a.x + i * a.stride;
+  T* dx = nullptr;
+  if constexpr (GRAD) dx = a.dx + i * a.dstride;
+  if (w == 0.0f) {
+    if (threadIdx.x == 0 && a.loss != nullptr) a.loss[i] = 0.0f;
+    if constexpr (GRAD) zero_row<T, NT>(dx, a.vocab);
+    return;
+  }
+  const Row<T, NT, NV> r(row, a.vocab);
+  float z[M], xj[M], pj[M];
+  int own[M];
   if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    float z[GRZ_MAX_TOP / 64];
     float zm = -INFINITY;
     bool any = false;
 #pragma unroll
-    for (int j = 0; j < GRZ_MAX_TOP / 64; ++j) {
-      const int e = j * 64 + lane;
+    for (int j = 0; j < M; ++j) {
+      const int q = j * 64 + static_cast<int>(threadIdx.x);
       z[j] = -INFINITY;
-      if (e < a.k) {
-        const int64_t at = i * a.k + e;
+      xj[j] = 0.0f;
+      own[j] = -1;
+      if (q < a.k) {
+        const int64_t at = i * a.k + q;
         const int64_t v = id_at(a.ids, a.id_bits, at);
-        const bool ok = v >= 0 && v < a.vocab;
         const float t = a.teacher_bf16 ? widen(static_cast<const uint16_t*>(a.teacher)[at])
                                        : static_cast<const float*>(a.teacher)[at];
-        if (ok) z[j] = t;
-        any = any || (ok && !(t == -INFINITY));
-        id[e] = ok ? static_cast<int32_t>(v) : -1;
+        if (v >= 0 && v < a.vocab) {
+          own[j] = static_cast<int>(v);
+          z[j] = t;
+          xj[j] = widen(row[v]);
+          any = any || !(t == -INFINITY);
+        }
+        id[q] = own[j];
       }
       zm = fmaxf(zm, z[j]);
     }
+    const bool some = __ballot(any) != 0;
     zm = wave_max(zm);
-    float sum = 0.0f, e[GRZ_MAX_TOP / 64];
-#pragma unroll
-    for (int j = 0; j < GRZ_MAX_TOP / 64; ++j) {
-      z[j] = (z[j] - zm) * a.inv_tau;
-      e[j] = j * 64 + lane < a.k ? __builtin_amdgcn_exp2f(z[j] * kLog2e) : 0.0f;
-      sum += e[j];
-    }
-    sum = wave_sum(sum);
-    const float logs = logf(sum), inv = 1.0f / sum;
-#pragma unroll
-    for (int j = 0; j < GRZ_MAX_TOP / 64; ++j) {
-      const int q = j * 64 + lane;
-      if (q < a.k) {
-        p[q] = e[j] * inv;
-        lp[q] = z[j] - logs;
-      }
-    }
-    if (lane == 0) listed = __ballot(any) != 0;
-    else (void)__ballot(any);
-  }
-  __syncthreads();
-  T* dx = nullptr;
-  if constexpr (GRAD) dx = a.dx + i * a.dstride;
-  if (w == 0.0f || !listed) {
-    if (threadIdx.x == 0 && a.loss != nullptr) a.loss[i] = 0.0f;
-    if constexpr (GRAD) zero_row(dx, a.vocab, NT);
-    return;
-  }
-  const Row<T, NT> r(row, a.vocab);
-  float m = -INFINITY;
-  r.each([&](float x, int) { m = fmaxf(m, x); });
-  m = block_max<NT>(m, lds);
-  float s = 0.0f;
-  const float l2 = kLog2e * a.inv_tau;
-  r.each([&](float x, int) { s += __builtin_amdgcn_exp2f((x - m) * l2); });
-  s = block_sum<NT>(s, lds);
-  const float logs = logf(s);
-  // The listed tokens: one thread each of the first GRZ_MAX_TOP.
-  float xj[GRZ_MAX_TOP / 64];
-  if (threadIdx.x < 64) {
     float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < GRZ_MAX_TOP / 64; ++j) {
-      const int e = j * 64 + static_cast<int>(threadIdx.x);
-      xj[j] = 0.0f;
-      if (e < a.k && id[e] >= 0) {
-        xj[j] = (widen(row[id[e]]) - m) * a.inv_tau - logs;
-        if (p[e] != 0.0f) sum += p[e] * (lp[e] - xj[j]);
-      }
+    for (int j = 0; j < M; ++j) {
+      z[j] = (z[j] - zm) * (kLog2e * a.inv_tau);
+      pj[j] = j * 64 + static_cast<int>(threadIdx.x) < a.k ? __builtin_amdgcn_exp2f(z[j]) : 0.0f;
+      sum += pj[j];
     }
     sum = wave_sum(sum);
-    if (threadIdx.x == 0 && a.loss != nullptr) a.loss[i] = w * a.tau * a.tau * sum;
+    const float log2z = log2f(sum), inv = 1.0f / sum;
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int q = j * 64 + static_cast<int>(threadIdx.x);
+      pj[j] *= inv;
+      z[j] -= log2z;
+      if (q < a.k) p[q] = pj[j];
+    }
+    if (threadIdx.x == 0) listed = some;
+  }
+  float m = -INFINITY;
+  r.each([&](float x, int) { m = fmaxf(m, x); });
+  if constexpr (NT == 64) __syncthreads();
+  m = block_max<NT>(m, lds_max);  // its barrier also publishes the list
+  if (!listed) {
+    if (threadIdx.x == 0 && a.loss != nullptr) a.loss[i] = 0.0f;
+    if constexpr (GRAD) zero_row<T, NT>(dx, a.vocab);
+    return;
+  }
+  const Exponent e(m, a.inv_tau);
+  float sum[1] = {0.0f};
+  each_exponent(r, e, [&](float d) { sum[0] += __builtin_amdgcn_exp2f(d); });
+  block_sum<NT, 1>(sum, lds_sum);  // its barrier stands between the last read and the first write
+  const float log2s = log2f(sum[0]);
+  const float c = w * a.grad_scale * a.tau;
+  if (threadIdx.x < 64) {
+    float part = 0.0f;
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      if (own[j] >= 0) {
+        if (pj[j] != 0.0f) part += pj[j] * (z[j] * kLn2 - e.log_q(xj[j], log2s));
+        xj[j] = e.of(xj[j]) - log2s;
+      }
+    }
+    part = wave_sum(part);
+    if (threadIdx.x == 0 && a.loss != nullptr) a.loss[i] = w * a.tau * a.tau * part;
   }
   if constexpr (GRAD) {
-    __syncthreads();  // in place: the listed elements have been read
-    const float c = w * a.grad_scale * a.tau;
-    const float log2s = logs * kLog2e;
-    r.map(dx, [&](float x) { return c * __builtin_amdgcn_exp2f((x - m) * l2 - log2s); });
+    map_exponent(r, dx, e, [&](float d) { return c * __builtin_amdgcn_exp2f(d - log2s); });
     __syncthreads();
     if (threadIdx.x < 64) {
 #pragma unroll
-      for (int j = 0; j < GRZ_MAX_TOP / 64; ++j) {
-        const int e = j * 64 + static_cast<int>(threadIdx.x);
-        if (e < a.k && id[e] >= 0) {
+      for (int j = 0; j < M; ++j) {
+        if (own[j] >= 0) {
           float target = 0.0f;
           bool first = true;
           for (int f = 0; f < a.k; ++f) {
-            if (id[f] == id[e]) {
+            if (id[f] == own[j]) {
               target += p[f];
-              first = first && f >= e;
+              first = first && f >= j * 64 + static_cast<int>(threadIdx.x);
             }
           }
-          if (first) put(dx + id[e], c * (__builtin_amdgcn_exp2f(xj[j] * kLog2e) - target));
+          if (first) put(dx + own[j], c * (__builtin_amdgcn_exp2f(xj[j]) - target));
         }
       }
     }
@@ -820,26 +1010,38 @@ __global__ __launch_bounds__(NT) void distill_kernel(DistillArgs<T> a) {
 }
 
 // One workgroup per row, kRowBatch rows per launch.
-template <typename T, bool GRAD>
-int logprob_launch(LogprobArgs<T> a, int64_t n, hipStream_t stream) {
+template <typename Args>
+int row_launch(void (*kernel)(Args), int threads, Args a, int64_t n, hipStream_t stream) {
   for (a.row0 = 0; a.row0 < n; a.row0 += kRowBatch) {
     const int64_t rows = n - a.row0 < kRowBatch ? n - a.row0 : kRowBatch;
-    const int st = launch(logprob_kernel<T, 256, GRAD>, dim3(static_cast<unsigned>(rows)),
-                          dim3(256), stream, a);
+    const int st = launch(kernel, dim3(static_cast<unsigned>(rows)), dim3(threads), stream, a);
     if (st != GRZ_OK) return st;
   }
   return GRZ_OK;
 }
 
+// Threads per row and kept vectors per thread, by the row's 16-byte vectors.
+#define GRZ_ROW_SHAPES(CALL)                                  \
+  const int64_t vectors = a.vocab / (16 / (int)sizeof(T));    \
+  if (vectors <= 64 * 4 && a.top <= 64) return CALL(64, 4);   \
+  if (vectors <= 256 * 8) return CALL(256, 8);                \
+  if (vectors <= 512 * 8) return CALL(512, 8);                \
+  if (vectors <= 1024 * 8) return CALL(1024, 8);              \
+  if (vectors <= 1024 * 16) return CALL(1024, 16);            \
+  return CALL(1024, 0);
+
 template <typename T, bool GRAD>
-int distill_launch(DistillArgs<T> a, int64_t n, hipStream_t stream) {
-  for (a.row0 = 0; a.row0 < n; a.row0 += kRowBatch) {
-    const int64_t rows = n - a.row0 < kRowBatch ? n - a.row0 : kRowBatch;
-    const int st = launch(distill_kernel<T, 256, GRAD>, dim3(static_cast<unsigned>(rows)),
-                          dim3(256), stream, a);
-    if (st != GRZ_OK) return st;
-  }
-  return GRZ_OK;
+int logprob_launch(const LogprobArgs<T>& a, int64_t n, hipStream_t stream) {
+#define GRZ_CALL(NT, NV) row_launch(logprob_kernel<T, NT, NV, GRAD>, NT, a, n, stream)
+  GRZ_ROW_SHAPES(GRZ_CALL)
+#undef GRZ_CALL
+}
+
+template <typename T, bool GRAD>
+int distill_launch(const DistillArgs<T>& a, int64_t n, hipStream_t stream) {
+#define GRZ_CALL(NT, NV) row_launch(distill_kernel<T, NT, NV, GRAD>, NT, a, n, stream)
+  GRZ_ROW_SHAPES(GRZ_CALL)
+#undef GRZ_CALL
 }
 
 // Whether dlogits may be written while logits are read: the same matrix, or
@@ -873,7 +1075,7 @@ int distill_run(const void* logits, int64_t n, int64_t vocab, int64_t stride, co
                 const float* weights, float grad_scale, float* loss, void* dlogits,
                 int64_t dstride, hipStream_t stream) {
   DistillArgs<T> a{0, static_cast<const T*>(logits), stride, static_cast<int>(vocab), ids, id_bits,
-                   teacher, teacher_dtype == GRZ_BF16, k, 1.0f / temperature, temperature,
+                   teacher, teacher_dtype == GRZ_BF16, k, 0, 1.0f / temperature, temperature,
                    grad_scale, weights, loss, static_cast<T*>(dlogits), dstride};
   return dlogits != nullptr ? distill_launch<T, true>(a, n, stream)
                             : distill_launch<T, false>(a, n, stream);
