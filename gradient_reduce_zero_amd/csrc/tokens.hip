@@ -197,6 +197,9 @@ __global__ __launch_bounds__(256) void lookup_kernel(const TI* __restrict__ tabl
 // The sort of the token ids: least significant digit first, stable, so that
 // equal ids end up in the order of their positions.  Ids outside [0, vocab)
 // get the key `vocab` and sort behind every row.
+//
+// The sort keeps few of the chip's CUs busy, so the launches that move pairs
+// carry workgroups behind their tiles' that write the table's zeros.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
@@ -220,6 +223,39 @@ __device__ __forceinline__ u32x2 sort_pair(const SortSrc& s, int64_t i) {
   return u32x2{key, static_cast<uint32_t>(i)};
 }
 
+// Rows [row0, row1) of the table to be zeroed, as bytes; `unit` is the widest
+// access that the rows' places and lengths allow (16, 8, 4 or 2 bytes).
+struct ZeroRows {
+  char* data;
+  int64_t stride, bytes;  // of a row
+  int64_t row0, row1;
+  int unit;
+};
+
+template <typename U>
+__device__ __forceinline__ void zero_units(const ZeroRows& z, int64_t first, int64_t step) {
+  const int64_t units = z.bytes / static_cast<int64_t>(sizeof(U));
+  const U zero = {};
+  for (int64_t r = z.row0 + first; r < z.row1; r += step) {
+    U* row = reinterpret_cast<U*>(z.data + r * z.stride);
+    for (int64_t c = threadIdx.x & 63; c < units; c += 64) row[c] = zero;
+  }
+}
+
+// One wave per row; `block` of `blocks` workgroups.
+__device__ __forceinline__ void zero_rows(const ZeroRows& z, int64_t block, int64_t blocks) {
+  const int waves = blockDim.x >> 6;
+  const int64_t first = block * waves + (threadIdx.x >> 6), step = blocks * waves;
+  if (z.unit == 16) zero_units<u32x4>(z, first, step);
+  else if (z.unit == 8) zero_units<u32x2>(z, first, step);
+  else if (z.unit == 4) zero_units<uint32_t>(z, first, step);
+  else zero_units<uint16_t>(z, first, step);
+}
+
+__global__ __launch_bounds__(256) void zero_rows_kernel(ZeroRows z) {
+  zero_rows(z, blockIdx.x, gridDim.x);
+}
+
 // counts[tile][digit] of one tile per workgroup.
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortSrc src, int64_t n,
                                                                   int shift, int bits,
@@ -238,52 +274,60 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortSrc src, i
     counts[static_cast<int64_t>(blockIdx.x) * digits + d] = hist[d];
 }
 
-// One pass: every pair of the tile goes to its place among all n.  Wave w of
-// the workgroup holds 64 * kSortItems consecutive pairs, 64 at a time; a
-// pair's rank among the equal digits before it in its wave comes from the
-// lanes' ballots of each digit bit.
-__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
-    SortSrc src, int64_t n, int shift, int bits, const uint32_t* __restrict__ counts,
-    u32x2* __restrict__ out) {
-  __shared__ uint32_t first[kDigits];                // where the tile's run of a digit begins
-  __shared__ uint16_t wave_count[kSortWaves][kDigits];  // then each wave's first rank in the tile
-  __shared__ uint32_t wave_sum[kSortWaves];
+// For many tiles: counts[tile][digit] becomes the pairs of the digit in earlier
+// tiles, totals[digit] their number in all.  A workgroup takes 64 digits, each
+// of its waves a run of tiles.
+__global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(uint32_t* __restrict__ counts,
+                                                                 uint32_t* __restrict__ totals,
+                                                                 int64_t tiles, int digits) {
+  __shared__ uint32_t sums[kSortWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int d = blockIdx.x * 64 + lane;
+  const int64_t share = ceil_div(tiles, kSortWaves);
+  const int64_t from = wave * share, to = from + share < tiles ? from + share : tiles;
+  uint32_t sum = 0;
+  if (d < digits) {
+#pragma unroll 8
+    for (int64_t t = from; t < to; ++t) sum += counts[t * digits + d];
+  }
+  sums[wave][lane] = sum;
+  __syncthreads();
+  uint32_t before = 0, total = 0;
+  for (int w = 0; w < kSortWaves; ++w) {
+    before += w < wave ? sums[w][lane] : 0u;
+    total += sums[w][lane];
+  }
+  if (d >= digits) return;
+  if (wave == 0) totals[d] = total;
+#pragma unroll 8
+  for (int64_t t = from; t < to; ++t) {
+    const uint32_t c = counts[t * digits + d];
+    counts[t * digits + d] = before;
+    before += c;
+  }
+}
+
+struct RankLds {
+  uint32_t wave_sum[kSortWaves];
+  uint32_t first[kDigits];                // where the tile's run of a digit begins
+  uint16_t before[kSortWaves][kDigits];   // the wave's first place in that run
+};
+
+// Places of the tile's pairs among its pairs of the same digit: lds.before of
+// the wave plus rank[j].  Wave w holds the kSortItems * 64 consecutive pairs
+// from w * kSortItems * 64 on, 64 at a time; a pair's rank among the equal
+// digits before it in its wave comes from the lanes' ballots of each digit bit.
+// Returns the tile's number of pairs of digit threadIdx.x.  Ends without a
+// barrier.
+__device__ __forceinline__ uint32_t tile_ranks(const u32x2 (&pair)[kSortItems], int64_t left,
+                                               int shift, int bits, RankLds& lds,
+                                               uint32_t (&rank)[kSortItems]) {
   const int digits = 1 << bits;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t tiles = ceil_div(n, kSortTile);
-  for (int w = 0; w < kSortWaves; ++w)
-    for (int d = tid; d < digits; d += kSortThreads) wave_count[w][d] = 0;
-  // Pairs of a digit in earlier tiles and in all; then the exclusive scan over the digits.
-  uint32_t before = 0, total = 0;
-  if (tid < digits) {
-    for (int64_t t = 0; t < tiles; ++t) {
-      const uint32_t c = counts[t * digits + tid];
-      before += t < blockIdx.x ? c : 0u;
-      total += c;
-    }
-  }
-  uint32_t scan = total;
-  for (int s = 1; s < 64; s <<= 1) {
-    const uint32_t o = __shfl_up(scan, s, 64);
-    scan += lane >= s ? o : 0u;
-  }
-  if (lane == 63) wave_sum[wave] = scan;
-  __syncthreads();
-  uint32_t wbase = 0;
-  for (int w = 0; w < wave; ++w) wbase += wave_sum[w];
-  if (tid < digits) first[tid] = wbase + scan - total + before;
-
-  u32x2 pair[kSortItems];
-  uint32_t rank[kSortItems];
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kSortTile + wave * 64 * kSortItems;
+  for (int d = lane; d < digits; d += 64) lds.before[wave][d] = 0;
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
-    const int64_t i = base + j * 64 + lane;
-    if (i < n) pair[j] = sort_pair(src, i);
-  }
-#pragma unroll
-  for (int j = 0; j < kSortItems; ++j) {
-    const bool in = base + j * 64 + lane < n;
+    const bool in = (wave * kSortItems + j) * 64 + lane < left;
     const uint32_t d = in ? (pair[j][0] >> shift) & (digits - 1) : 0u;
     uint64_t same = __ballot(in);
     for (int b = 0; b < bits; ++b) {
@@ -292,26 +336,166 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
     }
     const uint32_t earlier = static_cast<uint32_t>(__popcll(same & ((1ull << lane) - 1)));
     uint32_t r = 0;
-    if (in) r = wave_count[wave][d];
+    if (in) r = lds.before[wave][d];
     if (in && earlier == 0)
-      wave_count[wave][d] = static_cast<uint16_t>(r + static_cast<uint32_t>(__popcll(same)));
+      lds.before[wave][d] = static_cast<uint16_t>(r + static_cast<uint32_t>(__popcll(same)));
     rank[j] = r + earlier;
   }
   __syncthreads();
-  for (int d = tid; d < digits; d += kSortThreads) {
-    uint32_t sum = 0;
+  uint32_t sum = 0;
+  if (tid < digits) {
+    uint16_t c[kSortWaves];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) c[w] = lds.before[w][tid];
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = wave_count[w][d];
-      wave_count[w][d] = static_cast<uint16_t>(sum);
-      sum += c;
+      lds.before[w][tid] = static_cast<uint16_t>(sum);
+      sum += c[w];
     }
   }
+  return sum;
+}
+
+// lds.first[d] = pairs of smaller digits + `before`, from each thread's own
+// digit total.  Begins and ends with a barrier.
+__device__ __forceinline__ void digit_starts(uint32_t total, uint32_t before, int digits,
+                                             RankLds& lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t scan = total;
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const uint32_t o = __shfl_up(scan, s, 64);
+    scan += lane >= s ? o : 0u;
+  }
+  if (lane == 63) lds.wave_sum[wave] = scan;
   __syncthreads();
+  uint32_t base = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) base += w < wave ? lds.wave_sum[w] : 0u;
+  if (static_cast<int>(threadIdx.x) < digits) lds.first[threadIdx.x] = base + scan - total + before;
+  __syncthreads();
+}
+
+// All passes over at most one tile, in LDS, in one launch.
+__global__ __launch_bounds__(kSortThreads) void sort_tile_kernel(SortSrc src, int n, int passes,
+                                                                 int bits,
+                                                                 u32x2* __restrict__ out,
+                                                                 ZeroRows zero) {
+  __shared__ RankLds lds;
+  __shared__ u32x2 moved[kSortTile];
+  if (blockIdx.x > 0) {
+    zero_rows(zero, blockIdx.x - 1, gridDim.x - 1);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  u32x2 pair[kSortItems] = {};
+  uint32_t rank[kSortItems];
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
-    if (base + j * 64 + lane < n) {
+    const int i = (wave * kSortItems + j) * 64 + lane;
+    if (i < n) pair[j] = sort_pair(src, i);
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = pass * bits;
+    const uint32_t total = tile_ranks(pair, n, shift, bits, lds, rank);
+    digit_starts(total, 0, 1 << bits, lds);
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+      if ((wave * kSortItems + j) * 64 + lane < n) {
+        const uint32_t d = (pair[j][0] >> shift) & ((1u << bits) - 1);
+        const uint32_t at = lds.first[d] + lds.before[wave][d] + rank[j];
+        if (pass + 1 == passes) out[at] = pair[j];
+        else moved[at] = pair[j];
+      }
+    }
+    if (pass + 1 == passes) break;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+      const int i = (wave * kSortItems + j) * 64 + lane;
+      if (i < n) pair[j] = moved[i];
+    }
+  }
+}
+
+// One pass over several tiles, one workgroup each.  The number of each digit's
+// pairs in all and in the tiles before comes, with few tiles, from a count of
+// every pair by each workgroup itself (a launch less than a kernel that
+// counts); with more, from counts[tile][digit]; with many, from
+// sort_scan_kernel's.
+enum { kCountSelf, kCountTiles, kCountScanned };
+constexpr int kSelfTiles = 8, kDirectTiles = 64;
+constexpr int kHistCopies = 8;
+
+template <int MODE>
+__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
+    SortSrc src, int64_t n, int shift, int bits, const uint32_t* __restrict__ counts,
+    const uint32_t* __restrict__ totals, u32x2* __restrict__ out, ZeroRows zero) {
+  __shared__ RankLds lds;
+  const int64_t tiles = ceil_div(n, kSortTile), tile = blockIdx.x;
+  if (tile >= tiles) {
+    zero_rows(zero, tile - tiles, gridDim.x - tiles);
+    return;
+  }
+  const int digits = 1 << bits;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t base = tile * kSortTile;
+  u32x2 pair[kSortItems] = {};
+  uint32_t rank[kSortItems];
+#pragma unroll
+  for (int j = 0; j < kSortItems; ++j) {
+    const int64_t i = base + (wave * kSortItems + j) * 64 + lane;
+    if (i < n) pair[j] = sort_pair(src, i);
+  }
+  uint32_t before = 0, total = 0;
+  if constexpr (MODE == kCountSelf) {
+    // Neighbouring lanes add to different copies: ids of text crowd a few digits.
+    __shared__ uint32_t hist[kHistCopies][kDigits];
+    for (int d = tid; d < digits; d += kSortThreads) {
+#pragma unroll
+      for (int c = 0; c < kHistCopies; ++c) hist[c][d] = 0;
+    }
+    __syncthreads();
+    auto add = [&](int64_t from, int64_t to) {
+#pragma unroll 4
+      for (int64_t i = from + tid; i < to; i += kSortThreads)
+        atomicAdd(&hist[lane % kHistCopies][(sort_pair(src, i)[0] >> shift) & (digits - 1)], 1u);
+    };
+    auto sum = [&]() {
+      uint32_t v = 0;
+      if (tid < digits) {
+#pragma unroll
+        for (int c = 0; c < kHistCopies; ++c) v += hist[c][tid];
+      }
+      return v;
+    };
+    add(0, base);
+    __syncthreads();
+    before = sum();
+    __syncthreads();
+    add(base, n);
+    __syncthreads();
+    total = sum();
+  } else if constexpr (MODE == kCountTiles) {
+    if (tid < digits) {
+#pragma unroll 16
+      for (int64_t t = 0; t < tiles; ++t) {
+        const uint32_t c = counts[t * digits + tid];
+        before += t < tile ? c : 0u;
+        total += c;
+      }
+    }
+  } else if (tid < digits) {
+    before = counts[tile * digits + tid];
+    total = totals[tid];
+  }
+  tile_ranks(pair, n - base, shift, bits, lds, rank);
+  digit_starts(total, before, digits, lds);
+#pragma unroll
+  for (int j = 0; j < kSortItems; ++j) {
+    if (base + (wave * kSortItems + j) * 64 + lane < n) {
       const uint32_t d = (pair[j][0] >> shift) & (digits - 1);
-      out[first[d] + wave_count[wave][d] + rank[j]] = pair[j];
+      out[lds.first[d] + lds.before[wave][d] + rank[j]] = pair[j];
     }
   }
 }
@@ -323,110 +507,150 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
 // earlier chunk or goes on in the next leaves its sum in `partial`
 // (chunk, 0: began earlier; 1: begins here and goes on), which join_kernel
 // adds up in chunk order.
+//
+// A wave keeps the next kBatch rows on their way while it adds the last ones.
 
-constexpr int kChunk = 32;
+constexpr int kBatch = 8;
 
-template <typename TO>
-__device__ __forceinline__ float old_of(const TO* p) { return widen(*p); }
+template <typename T, int VEC> struct RawVec;  // a lane's part of a row as loaded
+template <> struct RawVec<uint16_t, 1> { uint16_t v; };
+template <> struct RawVec<float, 1> { float v; };
+template <> struct RawVec<uint16_t, 4> { u32x2 v; };
+template <> struct RawVec<float, 4> { u32x4 v; };
+
+template <typename T, int VEC>
+__device__ __forceinline__ void widen_vec(const RawVec<T, VEC>& r, float (&x)[VEC]) {
+  if constexpr (VEC == 1) {
+    x[0] = widen(r.v);
+  } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[2 * i] = __uint_as_float(r.v[i] << 16);
+      x[2 * i + 1] = __uint_as_float(r.v[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r.v[i]);
+  }
+}
 
 template <typename TO, int VEC>
-__device__ __forceinline__ void finish_row(TO* dst, float (&acc)[VEC], float scale,
+__device__ __forceinline__ void finish_row(TO* dst, const float (&acc)[VEC], float scale,
                                            int accumulate) {
+  float y[VEC];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) acc[i] *= scale;
+  for (int i = 0; i < VEC; ++i) y[i] = acc[i] * scale;
   if (accumulate) {
     float old[VEC];
     load_vec<TO, VEC>(dst, old);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] += old[i];
+    for (int i = 0; i < VEC; ++i) y[i] += old[i];
   }
-  store_vec<TO, VEC>(dst, acc);
-}
-
-template <typename TO, int VEC>
-__global__ __launch_bounds__(256) void zero_rows_kernel(TO* __restrict__ dst, int64_t stride,
-                                                        int64_t rows, int64_t dim) {
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (row >= rows) return;
-  float zero[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) zero[i] = 0.0f;
-  for (int64_t c = (threadIdx.x & 63) * VEC; c < dim; c += 64 * VEC)
-    store_vec<TO, VEC>(dst + row * stride + c, zero);
+  store_vec<TO, VEC>(dst, y);
 }
 
 template <typename TI, typename TO, int VEC>
 __global__ __launch_bounds__(64) void embed_grad_kernel(
     const TI* __restrict__ dout, int64_t istride, const u32x2* __restrict__ pairs, int64_t n,
-    uint32_t vocab, int64_t dim, float scale, int accumulate, float* __restrict__ partial,
-    TO* __restrict__ dtable, int64_t ostride) {
+    int size, uint32_t vocab, int64_t dim, float scale, int accumulate,
+    float* __restrict__ partial, TO* __restrict__ dtable, int64_t ostride) {
   const int lane = threadIdx.x;
   const int64_t chunk = blockIdx.x;
-  const int64_t base = chunk * kChunk;
-  const int cnt = static_cast<int>(n - base < kChunk ? n - base : kChunk);
-  u32x2 mine = {vocab, 0};
-  if (lane < cnt) mine = pairs[base + lane];
-  const uint32_t prev = base > 0 ? pairs[base - 1][0] : vocab;
-  const uint32_t next = base + cnt < n ? pairs[base + cnt][0] : vocab;
+  const int64_t base = chunk * size;
+  const int cnt = static_cast<int>(n - base < size ? n - base : size);
   const int64_t col = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * VEC;
   const bool on = col < dim;
+  const uint32_t prev = base > 0 ? pairs[base - 1][0] : vocab;
   float acc[VEC];
   bool begun = false;  // the current run began in this chunk
-  for (int e = 0; e < cnt; ++e) {
-    const uint32_t key = __builtin_amdgcn_readlane(mine[0], e);
-    if (key == vocab) break;  // nothing but ids of no row from here on
-    const uint32_t pos = __builtin_amdgcn_readlane(mine[1], e);
-    const uint32_t left = e > 0 ? __builtin_amdgcn_readlane(mine[0], e - 1) : prev;
-    const uint32_t right = e + 1 < cnt ? __builtin_amdgcn_readlane(mine[0], e + 1) : next;
-    float x[VEC];
-    if (on) load_vec<TI, VEC>(dout + static_cast<int64_t>(pos) * istride + col, x);
-    if (key != left || e == 0) {
-      begun = key != left;
+  uint32_t left = prev;
+  for (int part = 0; part < cnt; part += 64) {
+    // 64 pairs in the lanes, behind them the next one's key.
+    u32x2 mine = {vocab, 0};
+    if (part + lane < cnt) mine = pairs[base + part + lane];
+    const int here = cnt - part < 64 ? cnt - part : 64;
+    const uint32_t after = base + part + here < n ? pairs[base + part + here][0] : vocab;
+    RawVec<TI, VEC> raw[2][kBatch];
+    auto fetch = [&](int from, RawVec<TI, VEC> (&to)[kBatch]) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] = x[i];
-    } else {
+      for (int b = 0; b < kBatch; ++b) {
+        // Behind the last pair of a row: that pair's (nothing is read for ids of no row).
+        const int e = from + b < here ? from + b : here - 1;
+        const uint32_t pos = __builtin_amdgcn_readlane(mine[1], e);
+        const bool row = __builtin_amdgcn_readlane(mine[0], e) != vocab;
+        if (on && row)
+          to[b] = *reinterpret_cast<const RawVec<TI, VEC>*>(
+              dout + static_cast<int64_t>(pos) * istride + col);
+      }
+    };
+    auto add = [&](int from, const RawVec<TI, VEC> (&rows)[kBatch]) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] += x[i];
-    }
-    if (!on) continue;
-    if (!begun && (key != right || e + 1 == cnt)) {
-      store_vec<float, VEC>(partial + (chunk * 2) * dim + col, acc);
-    } else if (key != right) {
-      finish_row<TO, VEC>(dtable + static_cast<int64_t>(key) * ostride + col, acc, scale,
-                          accumulate);
-    } else if (e + 1 == cnt) {
-      store_vec<float, VEC>(partial + (chunk * 2 + 1) * dim + col, acc);
+      for (int b = 0; b < kBatch; ++b) {
+        const int e = from + b;
+        if (e >= here) break;
+        const uint32_t key = __builtin_amdgcn_readlane(mine[0], e);
+        if (key == vocab) break;  // nothing but ids of no row from here on
+        const uint32_t right = e + 1 < here ? __builtin_amdgcn_readlane(mine[0], e + 1) : after;
+        const bool last = part + e + 1 == cnt;
+        float x[VEC];
+        widen_vec<TI, VEC>(rows[b], x);
+        if (key != left || part + e == 0) {
+          begun = key != left;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[i] = x[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[i] += x[i];
+        }
+        left = key;
+        if (key == right && !last) continue;
+        if (!on) continue;
+        if (begun && key != right)
+          finish_row<TO, VEC>(dtable + static_cast<int64_t>(key) * ostride + col, acc, scale,
+                              accumulate);
+        else
+          store_vec<float, VEC>(partial + (chunk * 2 + (begun ? 1 : 0)) * dim + col, acc);
+      }
+    };
+    fetch(0, raw[0]);
+    for (int from = 0; from < here; from += 2 * kBatch) {
+      if (from + kBatch < here) fetch(from + kBatch, raw[1]);
+      add(from, raw[0]);
+      if (from + 2 * kBatch < here) fetch(from + 2 * kBatch, raw[0]);
+      if (from + kBatch < here) add(from + kBatch, raw[1]);
     }
   }
 }
 
 // One workgroup per (chunk border, column block); the border where a run first
-// crosses adds the whole run: its four waves take a quarter of the run's
-// partial sums each, in order, then the four in order.
+// crosses adds the whole run: its waves take equal parts of the run's partial
+// sums, in order, then the waves' sums in order.
+constexpr int kJoinWaves = 4;
+
 template <typename TO, int VEC>
-__global__ __launch_bounds__(256) void join_kernel(const u32x2* __restrict__ pairs, int64_t n,
-                                                   uint32_t vocab, int64_t dim, float scale,
-                                                   int accumulate,
-                                                   const float* __restrict__ partial,
-                                                   TO* __restrict__ dtable, int64_t ostride) {
-  __shared__ float part[4][64 * VEC];
+__global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(
+    const u32x2* __restrict__ pairs, int64_t n, int size, uint32_t vocab, int64_t dim, float scale,
+    int accumulate, const float* __restrict__ partial, TO* __restrict__ dtable, int64_t ostride) {
+  __shared__ float part[kJoinWaves][64 * VEC];
   const int64_t c = static_cast<int64_t>(blockIdx.x) + 1;  // border between chunks c - 1 and c
-  const uint32_t key = pairs[c * kChunk][0];
-  if (key == vocab || pairs[c * kChunk - 1][0] != key) return;
-  if (c > 1 && pairs[(c - 1) * kChunk - 1][0] == key) return;  // crossed an earlier border
+  const uint32_t key = pairs[c * size][0];
+  const uint32_t left = pairs[c * size - 1][0];
+  const uint32_t earlier = c > 1 ? pairs[(c - 1) * size - 1][0] : vocab;
+  if (key == vocab || left != key || earlier == key) return;  // no run, or from an earlier border
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   // The last chunk that begins with the key: 64 probes at a time.
-  const int64_t chunks = ceil_div(n, kChunk);
-  int64_t lo = c, hi = chunks;
+  int64_t lo = c, hi = ceil_div(n, size);
+  int64_t step = 1;  // runs are mostly short
   while (hi - lo > 1) {
-    const int64_t step = ceil_div(hi - lo, 64);
     const int64_t at = lo + lane * step;
-    const bool same = at < hi && pairs[at * kChunk][0] == key;
-    lo += (__popcll(__ballot(same)) - 1) * step;
-    hi = lo + step < hi ? lo + step : hi;
+    const bool same = at < hi && pairs[at * size][0] == key;
+    const int count = __popcll(__ballot(same));
+    lo += (count - 1) * step;
+    if (count < 64 && lo + step < hi) hi = lo + step;
+    step = ceil_div(hi - lo, 64);
   }
   const int64_t count = lo - c + 2;  // chunks c - 1 .. lo
-  const int64_t share = ceil_div(count, 4);
+  const int64_t share = ceil_div(count, kJoinWaves);
   const int64_t from = wave * share, to = from + share < count ? from + share : count;
   const int64_t col = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * VEC;
   const bool on = col < dim;
@@ -434,6 +658,7 @@ __global__ __launch_bounds__(256) void join_kernel(const u32x2* __restrict__ pai
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
   if (on) {
+#pragma unroll 8
     for (int64_t k = from; k < to; ++k) {
       float x[VEC];
       load_vec<float, VEC>(partial + ((c - 1 + k) * 2 + (k == 0 ? 1 : 0)) * dim + col, x);
@@ -446,9 +671,11 @@ __global__ __launch_bounds__(256) void join_kernel(const u32x2* __restrict__ pai
   __syncthreads();
   if (wave == 0 && on) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
-      acc[i] = ((part[0][lane * VEC + i] + part[1][lane * VEC + i]) +
-                part[2][lane * VEC + i]) + part[3][lane * VEC + i];
+    for (int i = 0; i < VEC; ++i) {
+      acc[i] = part[0][lane * VEC + i];
+#pragma unroll
+      for (int w = 1; w < kJoinWaves; ++w) acc[i] += part[w][lane * VEC + i];
+    }
     finish_row<TO, VEC>(dtable + static_cast<int64_t>(key) * ostride + col, acc, scale,
                         accumulate);
   }
@@ -1120,26 +1347,31 @@ int bits_of(int64_t v) {
 }
 
 // Workspace of the gradient: two arrays of pairs, the tiles' digit counts and
-// the chunks' partial sums, each on a 256-byte border.
+// the digits' totals, and the chunks' partial sums, each on a 256-byte border.
 struct GradPlan {
-  int passes, bits;
+  int passes, bits, chunk;
   int64_t tiles, chunks;
-  size_t pairs_a, pairs_b, counts, partial, total;
+  size_t pairs_b, counts, totals, partial, total;
 };
 
 size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+// Pairs per chunk: small ones give few ids enough waves, large ones keep the
+// partial sums of long runs few.
+int chunk_of(int64_t n) { return n <= 32768 ? 16 : n <= 131072 ? 32 : n <= 524288 ? 64 : 128; }
 
 GradPlan grad_plan(int64_t n, int64_t vocab, int64_t dim) {
   GradPlan p{};
   const int need = bits_of(vocab);  // keys 0 .. vocab
   p.passes = static_cast<int>(ceil_div(need, kMaxDigitBits));
   p.bits = static_cast<int>(ceil_div(need, p.passes));
+  p.chunk = chunk_of(n);
   p.tiles = ceil_div(n, kSortTile);
-  p.chunks = ceil_div(n, kChunk);
-  p.pairs_a = 0;
+  p.chunks = ceil_div(n, p.chunk);
   p.pairs_b = up256(static_cast<size_t>(n) * 8);
   p.counts = p.pairs_b + up256(static_cast<size_t>(n) * 8);
-  p.partial = p.counts + up256(static_cast<size_t>(p.tiles) * kDigits * 4);
+  p.totals = p.counts + up256(static_cast<size_t>(p.tiles) * kDigits * 4);
+  p.partial = p.totals + up256(kDigits * 4);
   p.total = p.partial + static_cast<size_t>(p.chunks) * 2 * static_cast<size_t>(dim) * 4;
   return p;
 }
@@ -1148,44 +1380,82 @@ GradPlan grad_plan(int64_t n, int64_t vocab, int64_t dim) {
 // accesses) or 1.
 template <typename T>
 bool vec_ok(const void* p, int64_t dim, int64_t stride, int vec) {
-  return dim % vec == 0 && stride % vec == 0 && aligned(p, sizeof(T) * vec < 16 ? sizeof(T) * vec : 16);
+  return dim % vec == 0 && stride % vec == 0 &&
+         aligned(p, sizeof(T) * vec < 16 ? sizeof(T) * vec : 16);
+}
+
+// Part `k` of `parts` of the rows of a table.
+template <typename T>
+ZeroRows zero_part(T* data, int64_t stride, int64_t rows, int64_t dim, int k, int parts) {
+  ZeroRows z{reinterpret_cast<char*>(data), stride * static_cast<int64_t>(sizeof(T)),
+             dim * static_cast<int64_t>(sizeof(T)), rows * k / parts, rows * (k + 1) / parts, 16};
+  const uint64_t at = reinterpret_cast<uintptr_t>(data) | static_cast<uint64_t>(z.bytes) |
+                      static_cast<uint64_t>(rows > 1 ? z.stride : 0);
+  while (at % z.unit) z.unit /= 2;
+  return z;
+}
+
+// Workgroups of `waves` waves for such a part: enough to fill the chip twice.
+unsigned zero_blocks(const ZeroRows& z, int waves) {
+  const int64_t want = ceil_div(z.row1 - z.row0, waves);
+  return static_cast<unsigned>(want < 512 ? want : 512);
 }
 
 template <typename TI, typename TO, int VEC>
 int embed_grad_launch(const TI* dout, int64_t istride, const void* ids, int id_bits, int64_t n,
                       int64_t vocab, int64_t dim, float scale, int accumulate, char* ws,
                       TO* dtable, int64_t ostride, hipStream_t stream) {
-  int st = GRZ_OK;
-  if (!accumulate) {
-    st = launch(zero_rows_kernel<TO, VEC>, dim3(static_cast<unsigned>(ceil_div(vocab, 4))),
-                dim3(256), stream, dtable, ostride, vocab, dim);
-    if (st != GRZ_OK) return st;
+  if (n == 0) {
+    if (accumulate) return GRZ_OK;
+    const ZeroRows z = zero_part(dtable, ostride, vocab, dim, 0, 1);
+    return launch(zero_rows_kernel, dim3(4 * zero_blocks(z, 4)), dim3(256), stream, z);
   }
-  if (n == 0) return GRZ_OK;
   const GradPlan p = grad_plan(n, vocab, dim);
-  u32x2* pairs[2] = {reinterpret_cast<u32x2*>(ws + p.pairs_a),
-                     reinterpret_cast<u32x2*>(ws + p.pairs_b)};
+  u32x2* pairs[2] = {reinterpret_cast<u32x2*>(ws), reinterpret_cast<u32x2*>(ws + p.pairs_b)};
   uint32_t* counts = reinterpret_cast<uint32_t*>(ws + p.counts);
+  uint32_t* totals = reinterpret_cast<uint32_t*>(ws + p.totals);
   float* partial = reinterpret_cast<float*>(ws + p.partial);
   SortSrc src{ids, id_bits, nullptr, static_cast<uint32_t>(vocab)};
-  const dim3 tiles(static_cast<unsigned>(p.tiles)), threads(kSortThreads);
-  for (int pass = 0; pass < p.passes; ++pass) {
-    const int shift = pass * p.bits;
-    st = launch(sort_count_kernel, tiles, threads, stream, src, n, shift, p.bits, counts);
+  const dim3 threads(kSortThreads);
+  const unsigned tiles = static_cast<unsigned>(p.tiles);
+  const int moves = p.tiles == 1 ? 1 : p.passes;  // launches that also write zeros
+  int st = GRZ_OK;
+  for (int k = 0; k < moves; ++k) {
+    const ZeroRows z = zero_part(dtable, ostride, accumulate ? 0 : vocab, dim, k, moves);
+    const dim3 grid(tiles + zero_blocks(z, kSortWaves));
+    const int shift = k * p.bits;
+    u32x2* out = pairs[k & 1];
+    if (p.tiles == 1) {
+      st = launch(sort_tile_kernel, grid, threads, stream, src, static_cast<int>(n), p.passes,
+                  p.bits, out, z);
+    } else if (p.tiles <= kSelfTiles) {
+      st = launch(sort_scatter_kernel<kCountSelf>, grid, threads, stream, src, n, shift, p.bits,
+                  counts, totals, out, z);
+    } else {
+      st = launch(sort_count_kernel, dim3(tiles), threads, stream, src, n, shift, p.bits, counts);
+      if (st != GRZ_OK) return st;
+      if (p.tiles <= kDirectTiles) {
+        st = launch(sort_scatter_kernel<kCountTiles>, grid, threads, stream, src, n, shift,
+                    p.bits, counts, totals, out, z);
+      } else {
+        st = launch(sort_scan_kernel, dim3(static_cast<unsigned>(ceil_div(1 << p.bits, 64))),
+                    threads, stream, counts, totals, p.tiles, 1 << p.bits);
+        if (st != GRZ_OK) return st;
+        st = launch(sort_scatter_kernel<kCountScanned>, grid, threads, stream, src, n, shift,
+                    p.bits, counts, totals, out, z);
+      }
+    }
     if (st != GRZ_OK) return st;
-    st = launch(sort_scatter_kernel, tiles, threads, stream, src, n, shift, p.bits, counts,
-                pairs[pass & 1]);
-    if (st != GRZ_OK) return st;
-    src = SortSrc{nullptr, 0, pairs[pass & 1], static_cast<uint32_t>(vocab)};
+    src = SortSrc{nullptr, 0, out, static_cast<uint32_t>(vocab)};
   }
   const unsigned slabs = static_cast<unsigned>(ceil_div(dim, 64 * VEC));
   st = launch(embed_grad_kernel<TI, TO, VEC>, dim3(static_cast<unsigned>(p.chunks), slabs),
-              dim3(64), stream, dout, istride, src.pairs, n, static_cast<uint32_t>(vocab), dim,
-              scale, accumulate, partial, dtable, ostride);
+              dim3(64), stream, dout, istride, src.pairs, n, p.chunk,
+              static_cast<uint32_t>(vocab), dim, scale, accumulate, partial, dtable, ostride);
   if (st != GRZ_OK || p.chunks == 1) return st;
-  return launch(join_kernel<TO, VEC>, dim3(static_cast<unsigned>(p.chunks - 1), slabs), dim3(256),
-                stream, src.pairs, n, static_cast<uint32_t>(vocab), dim, scale, accumulate,
-                partial, dtable, ostride);
+  return launch(join_kernel<TO, VEC>, dim3(static_cast<unsigned>(p.chunks - 1), slabs),
+                dim3(kJoinWaves * 64), stream, src.pairs, n, p.chunk,
+                static_cast<uint32_t>(vocab), dim, scale, accumulate, partial, dtable, ostride);
 }
 
 template <typename TI, typename TO>

@@ -147,6 +147,23 @@ def test_embed_grad_of_repeated_and_absent_ids(n, which):
     ref.assert_close(table, want, tol, which)
 
 
+@pytest.mark.parametrize("n", [8191, 32768, 32769, 40003, 131073, 262145, 300007, 524289, 700001])
+@pytest.mark.parametrize("vocab", [3, 700, 150000])
+def test_embed_grad_of_many_ids(n, vocab):
+    # Every way the digit counts are formed, every chunk length, runs over many
+    # chunks: a third of the ids the same, a tenth of no row.
+    dim = 4
+    ids = token_ids(n, vocab, 5)
+    u = torch.rand(n, device=DEV, generator=gen(7))
+    ids[u < 0.33] = vocab // 2
+    ids[u > 0.9] = -1
+    dout, _ = matrix(n, dim, F32, seed=4)
+    table, _ = matrix(vocab, dim, F32, seed=6)
+    grad_call(dout, ids, table, scale=0.5)
+    want, tol = ref.embed_grad(dout, ids, vocab, 0.5)
+    ref.assert_close(table, want, tol, "dtable")
+
+
 def test_embed_grad_bits_do_not_change_and_follow_the_rows():
     n, vocab, dim = 20011, 1000, 64
     dout, _ = matrix(n, dim, BF16, seed=10)
