@@ -37,12 +37,17 @@ template <typename T> struct NoDeduce { using type = T; };
 // dispatch counts its threads in 32 bits; the entry points' limits and
 // row_batches keep below that.
 template <typename... A>
-int launch(void (*kernel)(A...), dim3 grid, dim3 block, hipStream_t stream,
-           typename NoDeduce<A>::type... a) {
+int launch_lds(void (*kernel)(A...), size_t lds, dim3 grid, dim3 block, hipStream_t stream,
+               typename NoDeduce<A>::type... a) {
   if (static_cast<uint64_t>(grid.x) * block.x > UINT32_MAX) return GRZ_ERANGE;
   void* params[] = {static_cast<void*>(&a)...};
-  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, params, 0,
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, params, lds,
                          stream) == hipSuccess ? GRZ_OK : GRZ_EHIP;
+}
+template <typename... A>
+int launch(void (*kernel)(A...), dim3 grid, dim3 block, hipStream_t stream,
+           typename NoDeduce<A>::type... a) {
+  return launch_lds(kernel, 0, grid, block, stream, a...);
 }
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -194,19 +199,36 @@ __global__ __launch_bounds__(256) void lookup_kernel(const TI* __restrict__ tabl
 }
 
 // ---------------------------------------------------------------------------
-// The sort of the token ids: least significant digit first, stable, so that
-// equal ids end up in the order of their positions.  Ids outside [0, vocab)
-// get the key `vocab` and sort behind every row.
+// The sort of the token ids: stable, so that equal ids end up in the order of
+// their positions.  Ids outside [0, vocab) get the key `vocab` and sort behind
+// every row.  What a sort costs here is its launches' latency, so few of them:
 //
-// The sort keeps few of the chip's CUs busy, so the launches that move pairs
-// carry workgroups behind their tiles' that write the table's zeros.
+//  - up to kRankIds ids one launch: an id's place is the number of ids before
+//    it in the sorted order, counted by comparing it with all of them;
+//  - up to kMergeIds two: tiles of kMergeTile ids are sorted by that count,
+//    then an id's place is the sum of its places in all tiles, each found by a
+//    binary search in LDS;
+//  - beyond that a radix sort, least significant digit first, of a count and a
+//    scatter per pass; a workgroup of NT threads takes a tile of NT *
+//    kSortItems pairs: 1024 up to kSmallSort ids, so that they still spread
+//    over many CUs, 4096 beyond.
+//
+// The sort leaves HBM idle, so the launches that place pairs carry workgroups
+// behind their own that write the table's zeros.
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kRankIds = 4096;
+constexpr int kRankWaves = 16;
+constexpr int kRankLanes = 16;  // ids of a workgroup
+constexpr int kMergeIds = 32768;
+constexpr int kMergeTile = 256;
 constexpr int kSortItems = 4;
-constexpr int kSortTile = kSortThreads * kSortItems;
 constexpr int kMaxDigitBits = 9;
 constexpr int kDigits = 1 << kMaxDigitBits;
+constexpr int kBigSort = 1024, kLittleSort = 256;  // threads
+constexpr int64_t kSmallSort = 65536;
+constexpr int tile_of(int threads) { return threads * kSortItems; }
+// Behind the last id: larger than any key (vocab <= 2^26).
+constexpr uint32_t kNoKey = 0x7fffffffu;
 
 struct SortSrc {
   const void* ids;  // first pass: the tokens; later passes: null
@@ -257,33 +279,36 @@ __global__ __launch_bounds__(256) void zero_rows_kernel(ZeroRows z) {
 }
 
 // counts[tile][digit] of one tile per workgroup.
-__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortSrc src, int64_t n,
-                                                                  int shift, int bits,
-                                                                  uint32_t* __restrict__ counts) {
+template <int NT>
+__global__ __launch_bounds__(NT) void sort_count_kernel(SortSrc src, int64_t n, int shift,
+                                                        int bits, uint32_t* __restrict__ counts) {
   __shared__ uint32_t hist[kDigits];
   const int digits = 1 << bits;
-  for (int d = threadIdx.x; d < digits; d += kSortThreads) hist[d] = 0;
+  for (int d = threadIdx.x; d < digits; d += NT) hist[d] = 0;
   __syncthreads();
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kSortTile;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * tile_of(NT);
+#pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
-    const int64_t i = base + j * kSortThreads + threadIdx.x;
+    const int64_t i = base + j * NT + threadIdx.x;
     if (i < n) atomicAdd(&hist[(sort_pair(src, i)[0] >> shift) & (digits - 1)], 1u);
   }
   __syncthreads();
-  for (int d = threadIdx.x; d < digits; d += kSortThreads)
+  for (int d = threadIdx.x; d < digits; d += NT)
     counts[static_cast<int64_t>(blockIdx.x) * digits + d] = hist[d];
 }
 
 // For many tiles: counts[tile][digit] becomes the pairs of the digit in earlier
 // tiles, totals[digit] their number in all.  A workgroup takes 64 digits, each
 // of its waves a run of tiles.
-__global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(uint32_t* __restrict__ counts,
-                                                                 uint32_t* __restrict__ totals,
-                                                                 int64_t tiles, int digits) {
-  __shared__ uint32_t sums[kSortWaves][64];
+constexpr int kScanWaves = 16;
+
+__global__ __launch_bounds__(kScanWaves * 64) void sort_scan_kernel(uint32_t* __restrict__ counts,
+                                                                    uint32_t* __restrict__ totals,
+                                                                    int64_t tiles, int digits) {
+  __shared__ uint32_t sums[kScanWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int d = blockIdx.x * 64 + lane;
-  const int64_t share = ceil_div(tiles, kSortWaves);
+  const int64_t share = ceil_div(tiles, kScanWaves);
   const int64_t from = wave * share, to = from + share < tiles ? from + share : tiles;
   uint32_t sum = 0;
   if (d < digits) {
@@ -293,7 +318,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(uint32_t* __res
   sums[wave][lane] = sum;
   __syncthreads();
   uint32_t before = 0, total = 0;
-  for (int w = 0; w < kSortWaves; ++w) {
+  for (int w = 0; w < kScanWaves; ++w) {
     before += w < wave ? sums[w][lane] : 0u;
     total += sums[w][lane];
   }
@@ -307,21 +332,27 @@ __global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(uint32_t* __res
   }
 }
 
-struct RankLds {
-  uint32_t wave_sum[kSortWaves];
-  uint32_t first[kDigits];                // where the tile's run of a digit begins
-  uint16_t before[kSortWaves][kDigits];   // the wave's first place in that run
+// Digits of a workgroup's thread: D consecutive ones.
+template <int NT> constexpr int digits_each() { return kDigits > NT ? kDigits / NT : 1; }
+
+template <int NT> struct RankLds {
+  uint32_t wave_sum[NT / 64];
+  uint32_t first[kDigits];            // where the tile's run of a digit begins
+  uint16_t before[NT / 64][kDigits];  // the wave's first place in that run
 };
 
 // Places of the tile's pairs among its pairs of the same digit: lds.before of
 // the wave plus rank[j].  Wave w holds the kSortItems * 64 consecutive pairs
 // from w * kSortItems * 64 on, 64 at a time; a pair's rank among the equal
 // digits before it in its wave comes from the lanes' ballots of each digit bit.
-// Returns the tile's number of pairs of digit threadIdx.x.  Ends without a
-// barrier.
-__device__ __forceinline__ uint32_t tile_ranks(const u32x2 (&pair)[kSortItems], int64_t left,
-                                               int shift, int bits, RankLds& lds,
-                                               uint32_t (&rank)[kSortItems]) {
+// total: the tile's number of pairs of each of the thread's digits.  Ends
+// without a barrier.
+template <int NT>
+__device__ __forceinline__ void tile_ranks(const u32x2 (&pair)[kSortItems], int64_t left,
+                                           int shift, int bits, RankLds<NT>& lds,
+                                           uint32_t (&rank)[kSortItems],
+                                           uint32_t (&total)[digits_each<NT>()]) {
+  constexpr int D = digits_each<NT>();
   const int digits = 1 << bits;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int d = lane; d < digits; d += 64) lds.before[wave][d] = 0;
@@ -342,26 +373,35 @@ __device__ __forceinline__ uint32_t tile_ranks(const u32x2 (&pair)[kSortItems], 
     rank[j] = r + earlier;
   }
   __syncthreads();
-  uint32_t sum = 0;
-  if (tid < digits) {
-    uint16_t c[kSortWaves];
 #pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) c[w] = lds.before[w][tid];
+  for (int k = 0; k < D; ++k) {
+    const int d = tid * D + k;
+    uint32_t sum = 0;
+    if (d < digits) {
+      uint16_t c[NT / 64];
 #pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) {
-      lds.before[w][tid] = static_cast<uint16_t>(sum);
-      sum += c[w];
+      for (int w = 0; w < NT / 64; ++w) c[w] = lds.before[w][d];
+#pragma unroll
+      for (int w = 0; w < NT / 64; ++w) {
+        lds.before[w][d] = static_cast<uint16_t>(sum);
+        sum += c[w];
+      }
     }
+    total[k] = sum;
   }
-  return sum;
 }
 
 // lds.first[d] = pairs of smaller digits + `before`, from each thread's own
-// digit total.  Begins and ends with a barrier.
-__device__ __forceinline__ void digit_starts(uint32_t total, uint32_t before, int digits,
-                                             RankLds& lds) {
+// digits' totals.  Begins and ends with a barrier.
+template <int NT, int D>
+__device__ __forceinline__ void digit_starts(const uint32_t (&total)[D],
+                                             const uint32_t (&before)[D], int digits,
+                                             RankLds<NT>& lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t scan = total;
+  uint32_t own = 0;
+#pragma unroll
+  for (int k = 0; k < D; ++k) own += total[k];
+  uint32_t scan = own;
 #pragma unroll
   for (int s = 1; s < 64; s <<= 1) {
     const uint32_t o = __shfl_up(scan, s, 64);
@@ -369,77 +409,169 @@ __device__ __forceinline__ void digit_starts(uint32_t total, uint32_t before, in
   }
   if (lane == 63) lds.wave_sum[wave] = scan;
   __syncthreads();
-  uint32_t base = 0;
+  uint32_t start = scan - own;
 #pragma unroll
-  for (int w = 0; w < kSortWaves; ++w) base += w < wave ? lds.wave_sum[w] : 0u;
-  if (static_cast<int>(threadIdx.x) < digits) lds.first[threadIdx.x] = base + scan - total + before;
+  for (int w = 0; w < NT / 64; ++w) start += w < wave ? lds.wave_sum[w] : 0u;
+#pragma unroll
+  for (int k = 0; k < D; ++k) {
+    const int d = static_cast<int>(threadIdx.x) * D + k;
+    if (d < digits) lds.first[d] = start + before[k];
+    start += total[k];
+  }
   __syncthreads();
 }
 
-// All passes over at most one tile, in LDS, in one launch.
-__global__ __launch_bounds__(kSortThreads) void sort_tile_kernel(SortSrc src, int n, int passes,
-                                                                 int bits,
-                                                                 u32x2* __restrict__ out,
-                                                                 ZeroRows zero) {
-  __shared__ RankLds lds;
-  __shared__ u32x2 moved[kSortTile];
-  if (blockIdx.x > 0) {
-    zero_rows(zero, blockIdx.x - 1, gridDim.x - 1);
+// How many of the four keys are below `below`.  A difference's sign is shifted
+// into a word whose ones are counted: no lane masks, which a vector instruction
+// may only read some cycles after they are written.
+__device__ __forceinline__ uint32_t count_below(u32x4 k, uint32_t below) {
+  uint32_t signs = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) signs = __builtin_amdgcn_alignbit(signs, k[q] - below, 31);
+  return static_cast<uint32_t>(__popc(signs));
+}
+
+// The places of kRankLanes ids per workgroup among all n <= kRankIds.  The keys
+// lie in LDS; each wave compares its share of them with the ids, its lanes in
+// groups that take every G-th run of four keys.
+__global__ __launch_bounds__(kRankWaves * 64) void rank_kernel(SortSrc src, int n,
+                                                               u32x2* __restrict__ out,
+                                                               ZeroRows zero) {
+  constexpr int I = kRankLanes, G = 64 / I, kPart = kRankWaves * G * 4;
+  __shared__ u32x4 keys4[kRankIds / 4];
+  __shared__ uint32_t part[kRankWaves][64];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(keys4);
+  const int blocks = (n + I - 1) / I;
+  if (static_cast<int>(blockIdx.x) >= blocks) {
+    zero_rows(zero, blockIdx.x - blocks, gridDim.x - blocks);
     return;
   }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  u32x2 pair[kSortItems] = {};
-  uint32_t rank[kSortItems];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int padded = (n + kPart - 1) / kPart * kPart;
+  for (int j = threadIdx.x; j < padded; j += kRankWaves * 64)
+    keys[j] = j < n ? sort_pair(src, j)[0] : kNoKey;
+  __syncthreads();
+  const int first = blockIdx.x * I;          // a multiple of G * 4
+  const int i = first + lane % I, group = lane / I;
+  const uint32_t key = i < n ? keys[i] : 0u;
+  // Runs of G * 4 keys: in those before the workgroup's own ids an equal key counts.
+  const int runs = padded / (G * 4), own = first / (G * 4), share = runs / kRankWaves;
+  const int from = wave * share, to = from + share;
+  const int turn = own < from ? from : own < to ? own : to;
+  uint32_t count = 0;
+#pragma unroll 4
+  for (int r = from; r < turn; ++r) count += count_below(keys4[r * G + group], key + 1);
+#pragma unroll 4
+  for (int r = turn; r < to; ++r) count += count_below(keys4[r * G + group], key);
+  part[wave][lane] = count;
+  __syncthreads();
+  if (static_cast<int>(threadIdx.x) < I && i < n) {
+    uint32_t place = 0;
 #pragma unroll
-  for (int j = 0; j < kSortItems; ++j) {
-    const int i = (wave * kSortItems + j) * 64 + lane;
-    if (i < n) pair[j] = sort_pair(src, i);
+    for (int w = 0; w < kRankWaves; ++w) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) place += part[w][g * I + lane];
+    }
+    for (int m = 0; m < lane; ++m) place += keys[first + m] == key ? 1u : 0u;
+    out[place] = u32x2{key, static_cast<uint32_t>(i)};
   }
-  for (int pass = 0; pass < passes; ++pass) {
-    const int shift = pass * bits;
-    const uint32_t total = tile_ranks(pair, n, shift, bits, lds, rank);
-    digit_starts(total, 0, 1 << bits, lds);
+}
+
+// Sorts each tile of kMergeTile ids, one workgroup each, one id per thread.
+__global__ __launch_bounds__(kMergeTile) void sort_tiles_kernel(SortSrc src, int n,
+                                                                u32x2* __restrict__ out,
+                                                                ZeroRows zero) {
+  __shared__ u32x4 keys4[kMergeTile / 4];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(keys4);
+  const int tiles = (n + kMergeTile - 1) / kMergeTile;
+  if (static_cast<int>(blockIdx.x) >= tiles) {
+    zero_rows(zero, blockIdx.x - tiles, gridDim.x - tiles);
+    return;
+  }
+  const int tid = threadIdx.x, i = blockIdx.x * kMergeTile + tid;
+  const uint32_t key = i < n ? sort_pair(src, i)[0] : kNoKey;
+  keys[tid] = key;
+  __syncthreads();
+  // Runs of four keys before the wave's own 64 ids, its own, and behind them.
+  const int own = __builtin_amdgcn_readfirstlane(tid >> 6) * 16;
+  uint32_t place = 0;
+#pragma unroll 8
+  for (int r = 0; r < own; ++r) place += count_below(keys4[r], key + 1);
+#pragma unroll 4
+  for (int r = own; r < own + 16; ++r) {
+    const u32x4 k = keys4[r];
 #pragma unroll
-    for (int j = 0; j < kSortItems; ++j) {
-      if ((wave * kSortItems + j) * 64 + lane < n) {
-        const uint32_t d = (pair[j][0] >> shift) & ((1u << bits) - 1);
-        const uint32_t at = lds.first[d] + lds.before[wave][d] + rank[j];
-        if (pass + 1 == passes) out[at] = pair[j];
-        else moved[at] = pair[j];
-      }
-    }
-    if (pass + 1 == passes) break;
-    __syncthreads();
+    for (int q = 0; q < 4; ++q)
+      place += k[q] < key + (r * 4 + q < tid ? 1u : 0u) ? 1u : 0u;
+  }
+#pragma unroll 8
+  for (int r = own + 16; r < kMergeTile / 4; ++r) place += count_below(keys4[r], key);
+  if (i < n) out[blockIdx.x * kMergeTile + place] = u32x2{key, static_cast<uint32_t>(i)};
+}
+
+// Places the pairs of the sorted tiles among all n <= kMergeIds: 64 pairs of one
+// tile per workgroup, one per lane, each wave searching every 16th tile.
+__global__ __launch_bounds__(kRankWaves * 64) void merge_tiles_kernel(
+    const u32x2* __restrict__ pairs, int n, u32x2* __restrict__ out, ZeroRows zero) {
+  extern __shared__ uint32_t keys[];  // n, rounded up to whole tiles
+  __shared__ uint32_t part[kRankWaves][64];
+  const int blocks = (n + 63) / 64;
+  if (static_cast<int>(blockIdx.x) >= blocks) {
+    zero_rows(zero, blockIdx.x - blocks, gridDim.x - blocks);
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = (n + kMergeTile - 1) / kMergeTile;
+#pragma unroll 4
+  for (int j = threadIdx.x; j < tiles * kMergeTile; j += kRankWaves * 64)
+    keys[j] = j < n ? pairs[j][0] : kNoKey;
+  const int i = blockIdx.x * 64 + lane, own = blockIdx.x * 64 / kMergeTile;
+  u32x2 pair = {0, 0};
+  if (i < n) pair = pairs[i];
+  __syncthreads();
+  // Keys of tile t below the bound (an equal key of an earlier tile comes before).
+  uint32_t count = 0;
+#pragma unroll 4
+  for (int t = wave; t < tiles; t += kRankWaves) {
+    const uint32_t* tile = keys + t * kMergeTile;
+    const uint32_t below = pair[0] + (t < own ? 1u : 0u);
+    uint32_t at = 0;
 #pragma unroll
-    for (int j = 0; j < kSortItems; ++j) {
-      const int i = (wave * kSortItems + j) * 64 + lane;
-      if (i < n) pair[j] = moved[i];
-    }
+    for (int s = kMergeTile / 2; s > 0; s /= 2) at += tile[at + s - 1] < below ? s : 0;
+    at += tile[at] < below ? 1u : 0u;
+    count += t == own ? static_cast<uint32_t>(i - own * kMergeTile) : at;
+  }
+  part[wave][lane] = count;
+  __syncthreads();
+  if (wave == 0 && i < n) {
+    uint32_t place = 0;
+#pragma unroll
+    for (int w = 0; w < kRankWaves; ++w) place += part[w][lane];
+    out[place] = pair;
   }
 }
 
 // One pass over several tiles, one workgroup each.  The number of each digit's
-// pairs in all and in the tiles before comes, with few tiles, from a count of
-// every pair by each workgroup itself (a launch less than a kernel that
-// counts); with more, from counts[tile][digit]; with many, from
-// sort_scan_kernel's.
-enum { kCountSelf, kCountTiles, kCountScanned };
-constexpr int kSelfTiles = 8, kDirectTiles = 64;
-constexpr int kHistCopies = 8;
+// pairs in all and in the tiles before comes, with few tiles, straight from
+// counts[tile][digit], and with more from sort_scan_kernel's results.
+constexpr int kDirectTiles = 64;
 
-template <int MODE>
-__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
+template <int NT, bool SCANNED>
+__global__ __launch_bounds__(NT) void sort_scatter_kernel(
     SortSrc src, int64_t n, int shift, int bits, const uint32_t* __restrict__ counts,
     const uint32_t* __restrict__ totals, u32x2* __restrict__ out, ZeroRows zero) {
-  __shared__ RankLds lds;
-  const int64_t tiles = ceil_div(n, kSortTile), tile = blockIdx.x;
+  constexpr int D = digits_each<NT>();
+  __shared__ RankLds<NT> lds;
+  const int64_t tiles = ceil_div(n, tile_of(NT)), tile = blockIdx.x;
   if (tile >= tiles) {
     zero_rows(zero, tile - tiles, gridDim.x - tiles);
     return;
   }
   const int digits = 1 << bits;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t base = tile * kSortTile;
+  const int64_t base = tile * tile_of(NT);
   u32x2 pair[kSortItems] = {};
   uint32_t rank[kSortItems];
 #pragma unroll
@@ -447,50 +579,29 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
     const int64_t i = base + (wave * kSortItems + j) * 64 + lane;
     if (i < n) pair[j] = sort_pair(src, i);
   }
-  uint32_t before = 0, total = 0;
-  if constexpr (MODE == kCountSelf) {
-    // Neighbouring lanes add to different copies: ids of text crowd a few digits.
-    __shared__ uint32_t hist[kHistCopies][kDigits];
-    for (int d = tid; d < digits; d += kSortThreads) {
+  uint32_t before[D] = {}, total[D] = {}, mine[D];
+  if (tid * D < digits) {
+    if constexpr (SCANNED) {
 #pragma unroll
-      for (int c = 0; c < kHistCopies; ++c) hist[c][d] = 0;
-    }
-    __syncthreads();
-    auto add = [&](int64_t from, int64_t to) {
-#pragma unroll 4
-      for (int64_t i = from + tid; i < to; i += kSortThreads)
-        atomicAdd(&hist[lane % kHistCopies][(sort_pair(src, i)[0] >> shift) & (digits - 1)], 1u);
-    };
-    auto sum = [&]() {
-      uint32_t v = 0;
-      if (tid < digits) {
-#pragma unroll
-        for (int c = 0; c < kHistCopies; ++c) v += hist[c][tid];
+      for (int k = 0; k < D; ++k) {
+        if (tid * D + k >= digits) break;
+        before[k] = counts[tile * digits + tid * D + k];
+        total[k] = totals[tid * D + k];
       }
-      return v;
-    };
-    add(0, base);
-    __syncthreads();
-    before = sum();
-    __syncthreads();
-    add(base, n);
-    __syncthreads();
-    total = sum();
-  } else if constexpr (MODE == kCountTiles) {
-    if (tid < digits) {
+    } else {
 #pragma unroll 16
       for (int64_t t = 0; t < tiles; ++t) {
-        const uint32_t c = counts[t * digits + tid];
-        before += t < tile ? c : 0u;
-        total += c;
+#pragma unroll
+        for (int k = 0; k < D; ++k) {
+          const uint32_t c = tid * D + k < digits ? counts[t * digits + tid * D + k] : 0u;
+          before[k] += t < tile ? c : 0u;
+          total[k] += c;
+        }
       }
     }
-  } else if (tid < digits) {
-    before = counts[tile * digits + tid];
-    total = totals[tid];
   }
-  tile_ranks(pair, n - base, shift, bits, lds, rank);
-  digit_starts(total, before, digits, lds);
+  tile_ranks<NT>(pair, n - base, shift, bits, lds, rank, mine);
+  digit_starts<NT>(total, before, digits, lds);
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
     if (base + (wave * kSortItems + j) * 64 + lane < n) {
@@ -508,7 +619,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
 // (chunk, 0: began earlier; 1: begins here and goes on), which join_kernel
 // adds up in chunk order.
 //
-// A wave keeps the next kBatch rows on their way while it adds the last ones.
+// A wave's columns are P pieces of 64 * VEC, so that what it does per row (its
+// address, where runs end) is shared by up to 2 KB of it; the next kBatch rows
+// are on their way while the last ones are added.
 
 constexpr int kBatch = 8;
 
@@ -534,91 +647,129 @@ __device__ __forceinline__ void widen_vec(const RawVec<T, VEC>& r, float (&x)[VE
   }
 }
 
-template <typename TO, int VEC>
+// scale * acc, added to `old` (what the row holds) with ACC.
+template <bool ACC, typename TO, int VEC>
 __device__ __forceinline__ void finish_row(TO* dst, const float (&acc)[VEC], float scale,
-                                           int accumulate) {
+                                           const RawVec<TO, VEC>& old) {
   float y[VEC];
+  if constexpr (ACC) {
+    widen_vec<TO, VEC>(old, y);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) y[i] = acc[i] * scale;
-  if (accumulate) {
-    float old[VEC];
-    load_vec<TO, VEC>(dst, old);
+    for (int i = 0; i < VEC; ++i) y[i] = acc[i] * scale + y[i];
+  } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) y[i] += old[i];
+    for (int i = 0; i < VEC; ++i) y[i] = acc[i] * scale;
   }
   store_vec<TO, VEC>(dst, y);
 }
 
-template <typename TI, typename TO, int VEC>
+__device__ __forceinline__ int64_t lane_of(int64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(v), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(v >> 32), lane);
+  return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+template <typename TI, typename TO, int VEC, int P, bool ACC>
 __global__ __launch_bounds__(64) void embed_grad_kernel(
     const TI* __restrict__ dout, int64_t istride, const u32x2* __restrict__ pairs, int64_t n,
-    int size, uint32_t vocab, int64_t dim, float scale, int accumulate,
-    float* __restrict__ partial, TO* __restrict__ dtable, int64_t ostride) {
+    int size, uint32_t vocab, int64_t dim, float scale, float* __restrict__ partial,
+    TO* __restrict__ dtable, int64_t ostride) {
   const int lane = threadIdx.x;
   const int64_t chunk = blockIdx.x;
   const int64_t base = chunk * size;
   const int cnt = static_cast<int>(n - base < size ? n - base : size);
-  const int64_t col = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * VEC;
-  const bool on = col < dim;
-  const uint32_t prev = base > 0 ? pairs[base - 1][0] : vocab;
-  float acc[VEC];
-  bool begun = false;  // the current run began in this chunk
-  uint32_t left = prev;
-  for (int part = 0; part < cnt; part += 64) {
-    // 64 pairs in the lanes, behind them the next one's key.
-    u32x2 mine = {vocab, 0};
-    if (part + lane < cnt) mine = pairs[base + part + lane];
-    const int here = cnt - part < 64 ? cnt - part : 64;
-    const uint32_t after = base + part + here < n ? pairs[base + part + here][0] : vocab;
-    RawVec<TI, VEC> raw[2][kBatch];
-    auto fetch = [&](int from, RawVec<TI, VEC> (&to)[kBatch]) {
+  const int64_t col0 = static_cast<int64_t>(blockIdx.y) * (64 * VEC * P) + lane * VEC;
+  bool on[P];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        // Behind the last pair of a row: that pair's (nothing is read for ids of no row).
-        const int e = from + b < here ? from + b : here - 1;
-        const uint32_t pos = __builtin_amdgcn_readlane(mine[1], e);
-        const bool row = __builtin_amdgcn_readlane(mine[0], e) != vocab;
-        if (on && row)
-          to[b] = *reinterpret_cast<const RawVec<TI, VEC>*>(
-              dout + static_cast<int64_t>(pos) * istride + col);
-      }
-    };
-    auto add = [&](int from, const RawVec<TI, VEC> (&rows)[kBatch]) {
+  for (int k = 0; k < P; ++k) on[k] = col0 + k * 64 * VEC < dim;
+  uint32_t before = base > 0 ? pairs[base - 1][0] : vocab;
+  float acc[P][VEC] = {};
+  int slot = 0;       // where an unfinished run's sum goes: 0 while it began earlier
+  bool open = false;  // rows have been added since the last run's end
+  for (int part = 0; part < cnt; part += 64) {
+    const int here = cnt - part < 64 ? cnt - part : 64;
+    u32x2 mine = {vocab, 0};
+    if (lane < here) mine = pairs[base + part + lane];
+    const uint32_t after = base + part + here < n ? pairs[base + part + here][0] : vocab;
+    uint32_t right = __shfl_down(mine[0], 1, 64);
+    if (lane == here - 1) right = after;
+    const int rows = __popcll(__ballot(mine[0] != vocab));  // the ids of no row come last
+    const uint64_t ends = __ballot(mine[0] != right && mine[0] != vocab);
+    if (part == 0) slot = rows > 0 && __builtin_amdgcn_readlane(mine[0], 0) == before ? 0 : 1;
+    const int64_t in_at = static_cast<int64_t>(mine[1]) * istride;
+    const int64_t out_at = static_cast<int64_t>(mine[0]) * ostride;
+    struct Rows {
+      RawVec<TI, VEC> x[kBatch][P];
+      RawVec<TO, VEC> old[ACC ? kBatch : 1][P];  // what the rows hold where a run ends
+    } buf[2];
+    auto fetch = [&](int from, Rows& to) {
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         const int e = from + b;
-        if (e >= here) break;
-        const uint32_t key = __builtin_amdgcn_readlane(mine[0], e);
-        if (key == vocab) break;  // nothing but ids of no row from here on
-        const uint32_t right = e + 1 < here ? __builtin_amdgcn_readlane(mine[0], e + 1) : after;
-        const bool last = part + e + 1 == cnt;
-        float x[VEC];
-        widen_vec<TI, VEC>(rows[b], x);
-        if (key != left || part + e == 0) {
-          begun = key != left;
+        if (e >= rows) break;
+        const TI* src = dout + lane_of(in_at, e) + col0;
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) acc[i] = x[i];
-        } else {
+        for (int k = 0; k < P; ++k)
+          if (on[k]) to.x[b][k] = *reinterpret_cast<const RawVec<TI, VEC>*>(src + k * 64 * VEC);
+        if constexpr (ACC) {
+          if ((ends >> e) & 1) {
+            const TO* dst = dtable + lane_of(out_at, e) + col0;
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) acc[i] += x[i];
+            for (int k = 0; k < P; ++k)
+              if (on[k])
+                to.old[b][k] = *reinterpret_cast<const RawVec<TO, VEC>*>(dst + k * 64 * VEC);
+          }
         }
-        left = key;
-        if (key == right && !last) continue;
-        if (!on) continue;
-        if (begun && key != right)
-          finish_row<TO, VEC>(dtable + static_cast<int64_t>(key) * ostride + col, acc, scale,
-                              accumulate);
-        else
-          store_vec<float, VEC>(partial + (chunk * 2 + (begun ? 1 : 0)) * dim + col, acc);
       }
     };
-    fetch(0, raw[0]);
-    for (int from = 0; from < here; from += 2 * kBatch) {
-      if (from + kBatch < here) fetch(from + kBatch, raw[1]);
-      add(from, raw[0]);
-      if (from + 2 * kBatch < here) fetch(from + 2 * kBatch, raw[0]);
-      if (from + kBatch < here) add(from + kBatch, raw[1]);
+    auto add = [&](int from, const Rows& in) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int e = from + b;
+        if (e >= rows) break;
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          float x[VEC];
+          widen_vec<TI, VEC>(in.x[b][k], x);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[k][i] += x[i];
+        }
+        open = true;
+        if (!((ends >> e) & 1)) continue;
+        if (slot == 0) {
+          float* dst = partial + chunk * 2 * dim + col0;
+#pragma unroll
+          for (int k = 0; k < P; ++k)
+            if (on[k]) store_vec<float, VEC>(dst + k * 64 * VEC, acc[k]);
+        } else {
+          TO* dst = dtable + lane_of(out_at, e) + col0;
+#pragma unroll
+          for (int k = 0; k < P; ++k)
+            if (on[k])
+              finish_row<ACC, TO, VEC>(dst + k * 64 * VEC, acc[k], scale, in.old[ACC ? b : 0][k]);
+        }
+        slot = 1;
+        open = false;
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[k][i] = 0.0f;
+        }
+      }
+    };
+    fetch(0, buf[0]);
+    for (int from = 0; from < rows; from += 2 * kBatch) {
+      if (from + kBatch < rows) fetch(from + kBatch, buf[1]);
+      add(from, buf[0]);
+      if (from + 2 * kBatch < rows) fetch(from + 2 * kBatch, buf[0]);
+      if (from + kBatch < rows) add(from + kBatch, buf[1]);
     }
+  }
+  if (open) {
+    float* dst = partial + (chunk * 2 + slot) * dim + col0;
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+      if (on[k]) store_vec<float, VEC>(dst + k * 64 * VEC, acc[k]);
   }
 }
 
@@ -627,10 +778,10 @@ __global__ __launch_bounds__(64) void embed_grad_kernel(
 // sums, in order, then the waves' sums in order.
 constexpr int kJoinWaves = 4;
 
-template <typename TO, int VEC>
+template <typename TO, int VEC, bool ACC>
 __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(
     const u32x2* __restrict__ pairs, int64_t n, int size, uint32_t vocab, int64_t dim, float scale,
-    int accumulate, const float* __restrict__ partial, TO* __restrict__ dtable, int64_t ostride) {
+    const float* __restrict__ partial, TO* __restrict__ dtable, int64_t ostride) {
   __shared__ float part[kJoinWaves][64 * VEC];
   const int64_t c = static_cast<int64_t>(blockIdx.x) + 1;  // border between chunks c - 1 and c
   const uint32_t key = pairs[c * size][0];
@@ -654,6 +805,9 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(
   const int64_t from = wave * share, to = from + share < count ? from + share : count;
   const int64_t col = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * VEC;
   const bool on = col < dim;
+  TO* dst = dtable + static_cast<int64_t>(key) * ostride + col;
+  RawVec<TO, VEC> old;
+  if (ACC && wave == 0 && on) old = *reinterpret_cast<const RawVec<TO, VEC>*>(dst);
   float acc[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
@@ -676,8 +830,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(
 #pragma unroll
       for (int w = 1; w < kJoinWaves; ++w) acc[i] += part[w][lane * VEC + i];
     }
-    finish_row<TO, VEC>(dtable + static_cast<int64_t>(key) * ostride + col, acc, scale,
-                        accumulate);
+    finish_row<ACC, TO, VEC>(dst, acc, scale, old);
   }
 }
 
@@ -1350,6 +1503,7 @@ int bits_of(int64_t v) {
 // the digits' totals, and the chunks' partial sums, each on a 256-byte border.
 struct GradPlan {
   int passes, bits, chunk;
+  int threads;  // of a tile's workgroup
   int64_t tiles, chunks;
   size_t pairs_b, counts, totals, partial, total;
 };
@@ -1366,7 +1520,8 @@ GradPlan grad_plan(int64_t n, int64_t vocab, int64_t dim) {
   p.passes = static_cast<int>(ceil_div(need, kMaxDigitBits));
   p.bits = static_cast<int>(ceil_div(need, p.passes));
   p.chunk = chunk_of(n);
-  p.tiles = ceil_div(n, kSortTile);
+  p.threads = n <= kSmallSort ? kLittleSort : kBigSort;
+  p.tiles = ceil_div(n, tile_of(p.threads));
   p.chunks = ceil_div(n, p.chunk);
   p.pairs_b = up256(static_cast<size_t>(n) * 8);
   p.counts = p.pairs_b + up256(static_cast<size_t>(n) * 8);
@@ -1395,10 +1550,82 @@ ZeroRows zero_part(T* data, int64_t stride, int64_t rows, int64_t dim, int k, in
   return z;
 }
 
-// Workgroups of `waves` waves for such a part: enough to fill the chip twice.
+// Workgroups of `waves` waves for such a part: at most all the chip holds.
 unsigned zero_blocks(const ZeroRows& z, int waves) {
-  const int64_t want = ceil_div(z.row1 - z.row0, waves);
-  return static_cast<unsigned>(want < 512 ? want : 512);
+  const int64_t want = ceil_div(z.row1 - z.row0, waves), most = 8192 / waves;
+  return static_cast<unsigned>(want < most ? want : most);
+}
+
+// Sorts the ids into pairs (*sorted) and writes the table's zeros, which
+// zeros(k, parts) describes, beside it.
+template <typename Z>
+int rank_launch(const SortSrc& src, int64_t n, u32x2* pairs, Z zeros, hipStream_t stream) {
+  const ZeroRows z = zeros(0, 1);
+  const unsigned own = static_cast<unsigned>(ceil_div(n, kRankLanes));
+  return launch(rank_kernel, dim3(own + zero_blocks(z, kRankWaves)), dim3(kRankWaves * 64), stream,
+                src, static_cast<int>(n), pairs, z);
+}
+
+template <typename Z>
+int merge_launch(const SortSrc& src, int64_t n, u32x2* const (&pairs)[2], Z zeros,
+                 hipStream_t stream) {
+  const unsigned tiles = static_cast<unsigned>(ceil_div(n, kMergeTile));
+  const ZeroRows z0 = zeros(0, 2), z1 = zeros(1, 2);
+  const int st = launch(sort_tiles_kernel, dim3(tiles + zero_blocks(z0, kMergeTile / 64)),
+                        dim3(kMergeTile), stream, src, static_cast<int>(n), pairs[1], z0);
+  if (st != GRZ_OK) return st;
+  return launch_lds(merge_tiles_kernel, tiles * kMergeTile * 4,
+                    dim3(static_cast<unsigned>(ceil_div(n, 64)) + zero_blocks(z1, kRankWaves)),
+                    dim3(kRankWaves * 64), stream, pairs[1], static_cast<int>(n), pairs[0], z1);
+}
+
+template <int NT, typename Z>
+int sort_launch(SortSrc src, int64_t n, const GradPlan& p, u32x2* const (&pairs)[2],
+                uint32_t* counts, uint32_t* totals, Z zeros, const u32x2** sorted,
+                hipStream_t stream) {
+  const dim3 threads(NT);
+  const unsigned tiles = static_cast<unsigned>(p.tiles);
+  const int digits = 1 << p.bits, waves = NT / 64;
+  for (int k = 0; k < p.passes; ++k) {
+    const int shift = k * p.bits;
+    const ZeroRows z = zeros(k, p.passes);
+    const dim3 grid(tiles + zero_blocks(z, waves));
+    u32x2* out = pairs[k & 1];
+    int st = launch(sort_count_kernel<NT>, dim3(tiles), threads, stream, src, n, shift, p.bits,
+                    counts);
+    if (st == GRZ_OK && p.tiles <= kDirectTiles) {
+      st = launch(sort_scatter_kernel<NT, false>, grid, threads, stream, src, n, shift, p.bits,
+                  counts, totals, out, z);
+    } else if (st == GRZ_OK) {
+      st = launch(sort_scan_kernel, dim3(static_cast<unsigned>(ceil_div(digits, 64))),
+                  dim3(kScanWaves * 64), stream, counts, totals, p.tiles, digits);
+      if (st == GRZ_OK)
+        st = launch(sort_scatter_kernel<NT, true>, grid, threads, stream, src, n, shift, p.bits,
+                    counts, totals, out, z);
+    }
+    if (st != GRZ_OK) return st;
+    *sorted = out;
+    src = SortSrc{nullptr, 0, out, src.vocab};
+  }
+  return GRZ_OK;
+}
+
+// The kernel for `pieces` pieces of columns and the waves that share them: at
+// most as many a wave as its registers hold rows of on their way.
+template <typename TI, typename TO, int VEC, bool ACC>
+auto grad_kernel_for(int64_t pieces, int64_t* waves) {
+  constexpr int most = VEC == 1 ? 2 : (sizeof(TI) == 2 ? 4 : 2) / (ACC ? 2 : 1);
+  *waves = ceil_div(pieces, most);
+  const int each = static_cast<int>(ceil_div(pieces, *waves));
+  auto kernel = embed_grad_kernel<TI, TO, VEC, 1, ACC>;
+  if constexpr (most >= 2) {
+    if (each == 2) kernel = embed_grad_kernel<TI, TO, VEC, 2, ACC>;
+  }
+  if constexpr (most >= 4) {
+    if (each == 3) kernel = embed_grad_kernel<TI, TO, VEC, 3, ACC>;
+    if (each == 4) kernel = embed_grad_kernel<TI, TO, VEC, 4, ACC>;
+  }
+  return kernel;
 }
 
 template <typename TI, typename TO, int VEC>
@@ -1408,54 +1635,40 @@ int embed_grad_launch(const TI* dout, int64_t istride, const void* ids, int id_b
   if (n == 0) {
     if (accumulate) return GRZ_OK;
     const ZeroRows z = zero_part(dtable, ostride, vocab, dim, 0, 1);
-    return launch(zero_rows_kernel, dim3(4 * zero_blocks(z, 4)), dim3(256), stream, z);
+    return launch(zero_rows_kernel, dim3(zero_blocks(z, 4)), dim3(256), stream, z);
   }
   const GradPlan p = grad_plan(n, vocab, dim);
-  u32x2* pairs[2] = {reinterpret_cast<u32x2*>(ws), reinterpret_cast<u32x2*>(ws + p.pairs_b)};
+  u32x2* const pairs[2] = {reinterpret_cast<u32x2*>(ws),
+                           reinterpret_cast<u32x2*>(ws + p.pairs_b)};
   uint32_t* counts = reinterpret_cast<uint32_t*>(ws + p.counts);
   uint32_t* totals = reinterpret_cast<uint32_t*>(ws + p.totals);
   float* partial = reinterpret_cast<float*>(ws + p.partial);
-  SortSrc src{ids, id_bits, nullptr, static_cast<uint32_t>(vocab)};
-  const dim3 threads(kSortThreads);
-  const unsigned tiles = static_cast<unsigned>(p.tiles);
-  const int moves = p.tiles == 1 ? 1 : p.passes;  // launches that also write zeros
-  int st = GRZ_OK;
-  for (int k = 0; k < moves; ++k) {
-    const ZeroRows z = zero_part(dtable, ostride, accumulate ? 0 : vocab, dim, k, moves);
-    const dim3 grid(tiles + zero_blocks(z, kSortWaves));
-    const int shift = k * p.bits;
-    u32x2* out = pairs[k & 1];
-    if (p.tiles == 1) {
-      st = launch(sort_tile_kernel, grid, threads, stream, src, static_cast<int>(n), p.passes,
-                  p.bits, out, z);
-    } else if (p.tiles <= kSelfTiles) {
-      st = launch(sort_scatter_kernel<kCountSelf>, grid, threads, stream, src, n, shift, p.bits,
-                  counts, totals, out, z);
-    } else {
-      st = launch(sort_count_kernel, dim3(tiles), threads, stream, src, n, shift, p.bits, counts);
-      if (st != GRZ_OK) return st;
-      if (p.tiles <= kDirectTiles) {
-        st = launch(sort_scatter_kernel<kCountTiles>, grid, threads, stream, src, n, shift,
-                    p.bits, counts, totals, out, z);
-      } else {
-        st = launch(sort_scan_kernel, dim3(static_cast<unsigned>(ceil_div(1 << p.bits, 64))),
-                    threads, stream, counts, totals, p.tiles, 1 << p.bits);
-        if (st != GRZ_OK) return st;
-        st = launch(sort_scatter_kernel<kCountScanned>, grid, threads, stream, src, n, shift,
-                    p.bits, counts, totals, out, z);
-      }
-    }
-    if (st != GRZ_OK) return st;
-    src = SortSrc{nullptr, 0, out, static_cast<uint32_t>(vocab)};
-  }
-  const unsigned slabs = static_cast<unsigned>(ceil_div(dim, 64 * VEC));
-  st = launch(embed_grad_kernel<TI, TO, VEC>, dim3(static_cast<unsigned>(p.chunks), slabs),
-              dim3(64), stream, dout, istride, src.pairs, n, p.chunk,
-              static_cast<uint32_t>(vocab), dim, scale, accumulate, partial, dtable, ostride);
+  const SortSrc src{ids, id_bits, nullptr, static_cast<uint32_t>(vocab)};
+  auto zeros = [&](int k, int parts) {
+    return zero_part(dtable, ostride, accumulate ? 0 : vocab, dim, k, parts);
+  };
+  const u32x2* sorted = pairs[0];
+  int st;
+  if (n <= kRankIds) st = rank_launch(src, n, pairs[0], zeros, stream);
+  else if (n <= kMergeIds) st = merge_launch(src, n, pairs, zeros, stream);
+  else st = p.threads == kBigSort
+               ? sort_launch<kBigSort>(src, n, p, pairs, counts, totals, zeros, &sorted, stream)
+               : sort_launch<kLittleSort>(src, n, p, pairs, counts, totals, zeros, &sorted,
+                                          stream);
+  if (st != GRZ_OK) return st;
+  const int64_t pieces = ceil_div(dim, 64 * VEC);
+  int64_t waves = 0;
+  auto kernel = accumulate ? grad_kernel_for<TI, TO, VEC, true>(pieces, &waves)
+                           : grad_kernel_for<TI, TO, VEC, false>(pieces, &waves);
+  const uint32_t none = static_cast<uint32_t>(vocab);
+  st = launch(kernel, dim3(static_cast<unsigned>(p.chunks), static_cast<unsigned>(waves)),
+              dim3(64), stream, dout, istride, sorted, n, p.chunk, none, dim, scale, partial,
+              dtable, ostride);
   if (st != GRZ_OK || p.chunks == 1) return st;
-  return launch(join_kernel<TO, VEC>, dim3(static_cast<unsigned>(p.chunks - 1), slabs),
-                dim3(kJoinWaves * 64), stream, src.pairs, n, p.chunk,
-                static_cast<uint32_t>(vocab), dim, scale, accumulate, partial, dtable, ostride);
+  return launch(accumulate ? join_kernel<TO, VEC, true> : join_kernel<TO, VEC, false>,
+                dim3(static_cast<unsigned>(p.chunks - 1), static_cast<unsigned>(pieces)),
+                dim3(kJoinWaves * 64), stream, sorted, n, p.chunk, none, dim, scale, partial,
+                dtable, ostride);
 }
 
 template <typename TI, typename TO>

@@ -147,7 +147,7 @@ def test_embed_grad_of_repeated_and_absent_ids(n, which):
     ref.assert_close(table, want, tol, which)
 
 
-@pytest.mark.parametrize("n", [8191, 32768, 32769, 40003, 131073, 262145, 300007, 524289, 700001])
+@pytest.mark.parametrize("n", [255, 257, 4095, 4097, 8191, 16385, 32768, 32769, 40003, 131073, 262145, 300007, 524289, 700001])
 @pytest.mark.parametrize("vocab", [3, 700, 150000])
 def test_embed_grad_of_many_ids(n, vocab):
     # Every way the digit counts are formed, every chunk length, runs over many
