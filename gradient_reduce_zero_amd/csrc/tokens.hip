@@ -623,7 +623,7 @@ __global__ __launch_bounds__(NT) void sort_scatter_kernel(
 // address, where runs end) is shared by up to 2 KB of it; the next kBatch rows
 // are on their way while the last ones are added.
 
-constexpr int kBatch = 8;
+constexpr int kBatch = 4;
 
 template <typename T, int VEC> struct RawVec;  // a lane's part of a row as loaded
 template <> struct RawVec<uint16_t, 1> { uint16_t v; };
@@ -1510,16 +1510,22 @@ struct GradPlan {
 
 size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-// Pairs per chunk: small ones give few ids enough waves, large ones keep the
+// Pairs per chunk, a power of two from 8 to 128: short chunks give few rows
+// enough waves (some 2560 of them, a column piece each), long ones keep the
 // partial sums of long runs few.
-int chunk_of(int64_t n) { return n <= 32768 ? 16 : n <= 131072 ? 32 : n <= 524288 ? 64 : 128; }
+int chunk_of(int64_t n, int64_t dim) {
+  const int64_t want = n * ceil_div(dim, 256) / 2560;
+  int c = 8;
+  while (c < 128 && 2 * c <= want) c *= 2;
+  return c;
+}
 
 GradPlan grad_plan(int64_t n, int64_t vocab, int64_t dim) {
   GradPlan p{};
   const int need = bits_of(vocab);  // keys 0 .. vocab
   p.passes = static_cast<int>(ceil_div(need, kMaxDigitBits));
   p.bits = static_cast<int>(ceil_div(need, p.passes));
-  p.chunk = chunk_of(n);
+  p.chunk = chunk_of(n, dim);
   p.threads = n <= kSmallSort ? kLittleSort : kBigSort;
   p.tiles = ceil_div(n, tile_of(p.threads));
   p.chunks = ceil_div(n, p.chunk);
