@@ -1096,40 +1096,57 @@ __device__ __forceinline__ uint64_t order_of(float x, int index) {
 __device__ __forceinline__ int index_of(uint64_t order) {
   return static_cast<int>(0xffffffffu - static_cast<uint32_t>(order));
 }
-// The value of a key that is none of NaN's, at least -inf.
+// The value of a key (+0 for both zeros, a NaN for NaN's), at least -inf.
 __device__ __forceinline__ float value_of(uint32_t key) {
   if (key < 0x007fffffu) return -INFINITY;
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
 constexpr int kCandidates = 512;
-constexpr int kGroups = 256;
+constexpr int kGroups = 256, kFewGroups = 64;
 
 template <int NT> struct TopLds {
   static constexpr int G = NT < kGroups ? NT : kGroups;
   uint32_t group[G];
   uint64_t found[kCandidates];
-  uint32_t bound;
+  float bound;
   uint32_t count;
   uint64_t best[NT / 64];
 };
 
+// A value (of key c) that at least `top` of the wave's M * 64 keys are not
+// below, and few more: the keys' upper 16 bits, found bit by bit.
+template <int M>
+__device__ __forceinline__ uint32_t bound_of(const uint32_t (&k)[M], int top) {
+  uint32_t bound = 0;
+#pragma unroll
+  for (int b = 31; b >= 16; --b) {
+    const uint32_t c = bound | (1u << b);
+    int have = 0;
+#pragma unroll
+    for (int i = 0; i < M; ++i) have += __popcll(__ballot(k[i] >= c));
+    if (have >= top) bound = c;
+  }
+  return bound;
+}
+
 // The `top` elements that come first, handed to emit(place, order).
 //
-// The largest elements of G groups of threads (a thread, or a few neighbours)
-// are found first: the top-th largest of those bounds the list from below, and
-// few elements lie at or above it.  They are gathered and each finds its place
-// by counting the ones before it.  The bound is searched over the keys' upper
-// 16 bits.  A row with more candidates than fit (many equal values), or with
-// NaN, takes one search over the row per place instead.
+// The largest elements of G groups of threads are found first: the top-th
+// largest of those bounds the list from below, and few elements lie at or above
+// it.  They are gathered and each finds its place by counting the ones before
+// it.  G is 64 for short lists and 256 for long ones, so that the bound stays
+// well inside the groups' maxima.  A row with more candidates than fit (many
+// equal values), or with NaN, takes one search over the row per place instead.
 //
 // own_max: the largest of the thread's elements; exact: the row holds no NaN.
 template <typename T, int NT, int NV, bool ONCE, typename F>
 __device__ __forceinline__ void top_of(const Row<T, NT, NV, ONCE>& r, int vocab, float own_max,
                                        bool exact, int top, TopLds<NT>& lds, F emit) {
-  constexpr int G = TopLds<NT>::G;
+  constexpr int G = TopLds<NT>::G, E = Row<T, NT, NV, ONCE>::E;
   const int lane = threadIdx.x & 63;
   if (exact && top <= G) {
+    const bool few = G > kFewGroups && top <= kFewGroups / 2;
     float g = own_max;
     if constexpr (NT / G >= 2) g = fmaxf(g, lane_swap<kSwap1>(g));
     if constexpr (NT / G >= 4) g = fmaxf(g, lane_swap<kSwap2>(g));
@@ -1141,25 +1158,36 @@ __device__ __forceinline__ void top_of(const Row<T, NT, NV, ONCE>& r, int vocab,
       uint32_t k[G / 64];
 #pragma unroll
       for (int i = 0; i < G / 64; ++i) k[i] = lds.group[i * 64 + lane];
-      uint32_t bound = 0;
-      for (int b = 31; b >= 16; --b) {
-        const uint32_t c = bound | (1u << b);
-        int have = 0;
+      uint32_t bound;
+      if (few) {
+        uint32_t most[1] = {k[0]};
 #pragma unroll
-        for (int i = 0; i < G / 64; ++i) have += __popcll(__ballot(k[i] >= c));
-        if (have >= top) bound = c;
+        for (int i = 1; i < G / 64; ++i) most[0] = k[i] > most[0] ? k[i] : most[0];
+        bound = bound_of<1>(most, top);
+      } else {
+        bound = bound_of<G / 64>(k, top);
       }
-      if (lane == 0) lds.bound = bound;
+      if (lane == 0) lds.bound = value_of(bound);
     }
     __syncthreads();
-    const float bound = value_of(lds.bound);
+    const float bound = lds.bound;
     if (own_max >= bound) {
-      r.each([&](float x, int index) {
+      auto check = [&](float x, int index) {
         if (x >= bound) {
           const uint32_t at = atomicAdd(&lds.count, 1u);
           if (at < kCandidates) lds.found[at] = order_of(x, index);
         }
+      };
+      r.vectors([&](float (&x)[E], int at) {
+        float most = x[0];
+#pragma unroll
+        for (int i = 1; i < E; ++i) most = fmaxf(most, x[i]);
+        if (most >= bound) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) check(x[i], at + i);
+        }
       });
+      if (r.edge >= 0) check(r.edge_x, r.edge);
     }
     __syncthreads();
     const int count = static_cast<int>(lds.count);
@@ -1167,6 +1195,7 @@ __device__ __forceinline__ void top_of(const Row<T, NT, NV, ONCE>& r, int vocab,
       for (int c = threadIdx.x; c < count; c += NT) {
         const uint64_t mine = lds.found[c];
         int place = 0;
+#pragma unroll 8
         for (int o = 0; o < count; ++o) place += lds.found[o] > mine ? 1 : 0;
         if (place < top) emit(place, mine);
       }
@@ -1264,9 +1293,9 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void logprob_kernel(LogprobArgs
   } else if (a.top > 0) {
     __shared__ TopLds<NT> lds_top;
     top_of(r, a.vocab, own_max, sum[0] == sum[0], a.top, lds_top, [&](int place, uint64_t order) {
-      const int index = index_of(order);
-      a.top_ids[i * a.top + place] = index;
-      a.top_logprobs[i * a.top + place] = e.log_q(widen(row[index]), log2s);
+      a.top_ids[i * a.top + place] = index_of(order);
+      a.top_logprobs[i * a.top + place] =
+          e.log_q(value_of(static_cast<uint32_t>(order >> 32)), log2s);
     });
   }
 }
