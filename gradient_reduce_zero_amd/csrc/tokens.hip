@@ -886,6 +886,11 @@ template <typename T, int NT, int NV, bool ONCE = false> struct Row {
     }
     edge_x = edge >= 0 ? widen(p[edge]) : 0.0f;
   }
+  // The thread that holds (and in map() stores) an element.
+  __device__ __forceinline__ int owner(int index) const {
+    const int in = index - head, v = in / E;
+    return in < 0 ? index : v < nvec ? v % NT : in - nvec * E + head;
+  }
   static __device__ __forceinline__ void unpack(u32x4 u, float (&x)[E]) {
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -1102,6 +1107,12 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
+// What waves read of each other's LDS writes without a barrier is their own.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // The top list.  The largest elements of G groups of threads are found first:
 // the top-th largest of those bounds the list from below, and few elements lie
 // at or above it.  They are gathered and each finds its place by counting the
@@ -1205,12 +1216,6 @@ __device__ __forceinline__ void add_candidates(const float (&x)[E], int at, floa
       ++place;
     }
   }
-}
-
-// What waves read of each other's LDS writes without a barrier is their own.
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
 }
 
 // Third step, behind a barrier: the `top` elements that come first, handed to
@@ -1361,10 +1366,9 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void logprob_kernel(LogprobArgs
       return -__builtin_amdgcn_exp2f(lq) * fmaf(slope, fmaxf(lq, kLowest), base);
     };
     map_exponent(r, dx, e, value);
-    if (given) {
-      __syncthreads();
-      if (threadIdx.x == 0) put(dx + target, glp + value(e.of(xt)));
-    }
+    // Over what its thread has just stored.
+    if (given && r.owner(static_cast<int>(target)) == static_cast<int>(threadIdx.x))
+      put(dx + target, glp + value(e.of(xt)));
   } else if (a.top > 0) {
     if (NT == 64) __syncthreads();
     top_list(r, a.vocab, own_max, sum[0] == sum[0], a.top, lds_top, [&](int place, uint64_t order) {
@@ -1397,16 +1401,40 @@ template <typename T> struct DistillArgs {
 
 // p = softmax over the listed z / tau, q = softmax over the row of x / tau:
 // loss = w tau^2 sum_j p_j (log p_j - log q_j), dx = w c tau (q - p).
-// The first wave holds the list, two entries per lane.
+//
+// The first wave holds the list, two entries per lane; its loads go out before
+// the row's, so that the list is ready when the row comes.  A listed element's
+// gradient is stored by the thread that holds it, over what it has stored
+// before: a thread finds its entries through `mail`, and no wave has to wait for
+// another's stores.
 template <typename T, int NT, int NV, bool GRAD>
 __global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs<T> a) {
-  constexpr int M = GRZ_MAX_TOP / 64;
+  constexpr int M = GRZ_MAX_TOP / 64, kNone = 255;
   __shared__ float lds_max[NT / 64];
   __shared__ float lds_sum[NT / 64][1];
   __shared__ int32_t id[GRZ_MAX_TOP];
-  __shared__ float p[GRZ_MAX_TOP];
+  __shared__ float p[GRZ_MAX_TOP];       // of the entry; behind the barrier, of its token
+  __shared__ float xl[GRZ_MAX_TOP];
+  __shared__ int mail[GRAD ? NT : 1];    // a thread's first entry
+  __shared__ int next[GRZ_MAX_TOP];      // the same thread's next one
   __shared__ int listed;
   const int64_t i = a.row0 + blockIdx.x;
+  const int lane = threadIdx.x & 63;
+  int64_t v[M];
+  float z[M];
+  if (threadIdx.x < 64) {
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      v[j] = -1;
+      z[j] = -INFINITY;
+      if (j * 64 + lane < a.k) {
+        const int64_t at = i * a.k + j * 64 + lane;
+        v[j] = id_at(a.ids, a.id_bits, at);
+        z[j] = a.teacher_bf16 ? widen(static_cast<const uint16_t*>(a.teacher)[at])
+                              : static_cast<const float*>(a.teacher)[at];
+      }
+    }
+  }
   const float w = a.weights != nullptr ? a.weights[i] : 1.0f;
   const T* row = a.x + i * a.stride;
   T* dx = nullptr;
@@ -1417,30 +1445,20 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs
     return;
   }
   const Row<T, NT, NV, !GRAD> r(row, a.vocab);
-  float z[M], xj[M], pj[M];
-  int own[M];
+  if constexpr (GRAD) mail[threadIdx.x] = kNone;
+  float xj[M], pj[M];
   if (threadIdx.x < 64) {
     float zm = -INFINITY;
     bool any = false;
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const int q = j * 64 + static_cast<int>(threadIdx.x);
-      z[j] = -INFINITY;
-      xj[j] = 0.0f;
-      own[j] = -1;
-      if (q < a.k) {
-        const int64_t at = i * a.k + q;
-        const int64_t v = id_at(a.ids, a.id_bits, at);
-        const float t = a.teacher_bf16 ? widen(static_cast<const uint16_t*>(a.teacher)[at])
-                                       : static_cast<const float*>(a.teacher)[at];
-        if (v >= 0 && v < a.vocab) {
-          own[j] = static_cast<int>(v);
-          z[j] = t;
-          xj[j] = widen(row[v]);
-          any = any || !(t == -INFINITY);
-        }
-        id[q] = own[j];
+      const bool ok = v[j] >= 0 && v[j] < a.vocab;
+      xj[j] = ok ? widen(row[v[j]]) : 0.0f;
+      if (!ok) {
+        v[j] = -1;
+        z[j] = -INFINITY;
       }
+      any = any || !(z[j] == -INFINITY);
       zm = fmaxf(zm, z[j]);
     }
     const bool some = __ballot(any) != 0;
@@ -1449,19 +1467,22 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs
 #pragma unroll
     for (int j = 0; j < M; ++j) {
       z[j] = (z[j] - zm) * (kLog2e * a.inv_tau);
-      pj[j] = j * 64 + static_cast<int>(threadIdx.x) < a.k ? __builtin_amdgcn_exp2f(z[j]) : 0.0f;
+      pj[j] = v[j] >= 0 ? __builtin_amdgcn_exp2f(z[j]) : 0.0f;
       sum += pj[j];
     }
     sum = wave_sum(sum);
     const float log2z = log2f(sum), inv = 1.0f / sum;
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      const int q = j * 64 + static_cast<int>(threadIdx.x);
+      const int q = j * 64 + lane;
       pj[j] *= inv;
       z[j] -= log2z;
-      if (q < a.k) p[q] = pj[j];
+      if (GRAD && q < a.k) {
+        id[q] = static_cast<int32_t>(v[j]);
+        p[q] = pj[j];
+      }
     }
-    if (threadIdx.x == 0) listed = some;
+    if (lane == 0) listed = some;
   }
   float m = -INFINITY;
   r.each([&](float x, int) { m = fmaxf(m, x); });
@@ -1472,43 +1493,60 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs
     if constexpr (GRAD) zero_row<T, NT>(dx, a.vocab);
     return;
   }
-  const Exponent e(m, a.inv_tau);
-  float sum[1] = {0.0f};
-  each_exponent(r, e, [&](float d) { sum[0] += __builtin_amdgcn_exp2f(d); });
-  block_sum<NT, 1>(sum, lds_sum);  // its barrier stands between the last read and the first write
-  const float log2s = log2f(sum[0]);
-  const float c = w * a.grad_scale * a.tau;
-  if (threadIdx.x < 64) {
-    float part = 0.0f;
+  // By the last wave, which has the fewest vectors, beside the exponentials:
+  // each listed token's whole p, in its first entry, and who stores it.
+  if (GRAD && threadIdx.x >= NT - 64) {
+    float all[M];
+    bool first[M];
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-      if (own[j] >= 0) {
-        if (pj[j] != 0.0f) part += pj[j] * (z[j] * kLn2 - e.log_q(xj[j], log2s));
-        xj[j] = e.of(xj[j]) - log2s;
-      }
-    }
-    part = wave_sum(part);
-    if (threadIdx.x == 0 && a.loss != nullptr) a.loss[i] = w * a.tau * a.tau * part;
-  }
-  if constexpr (GRAD) {
-    map_exponent(r, dx, e, [&](float d) { return c * __builtin_amdgcn_exp2f(d - log2s); });
-    __syncthreads();
-    if (threadIdx.x < 64) {
-#pragma unroll
-      for (int j = 0; j < M; ++j) {
-        if (own[j] >= 0) {
-          float target = 0.0f;
-          bool first = true;
-          for (int f = 0; f < a.k; ++f) {
-            if (id[f] == own[j]) {
-              target += p[f];
-              first = first && f >= j * 64 + static_cast<int>(threadIdx.x);
-            }
+      const int q = j * 64 + lane;
+      first[j] = q < a.k && id[q] >= 0;
+      all[j] = 0.0f;
+      if (first[j]) {
+        for (int f = 0; f < a.k; ++f) {
+          if (id[f] == id[q]) {
+            all[j] += p[f];
+            first[j] = first[j] && f >= q;
           }
-          if (first) put(dx + own[j], c * (__builtin_amdgcn_exp2f(xj[j]) - target));
         }
       }
     }
+    wave_fence();
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int q = j * 64 + lane;
+      if (first[j]) {
+        p[q] = all[j];
+        next[q] = atomicExch(&mail[r.owner(id[q])], q);
+      }
+    }
+  }
+  const Exponent e(m, a.inv_tau);
+  float sum[1] = {0.0f};
+  each_exponent(r, e, [&](float d) { sum[0] += __builtin_amdgcn_exp2f(d); });
+  if (GRAD && threadIdx.x < 64) {
+#pragma unroll
+    for (int j = 0; j < M; ++j)
+      if (j * 64 + lane < a.k) xl[j * 64 + lane] = xj[j];
+  }
+  if constexpr (NT == 64) __syncthreads();
+  block_sum<NT, 1>(sum, lds_sum);  // its barrier stands between the last read and the first write
+  const float log2s = log2f(sum[0]);
+  if (threadIdx.x < 64 && a.loss != nullptr) {
+    float part = 0.0f;
+#pragma unroll
+    for (int j = 0; j < M; ++j)
+      if (pj[j] != 0.0f) part += pj[j] * (z[j] * kLn2 - e.log_q(xj[j], log2s));
+    part = wave_sum(part);
+    if (lane == 0) a.loss[i] = w * a.tau * a.tau * part;
+  }
+  if constexpr (GRAD) {
+    const float c = w * a.grad_scale * a.tau;
+    auto q_of = [&](float d) { return __builtin_amdgcn_exp2f(d - log2s); };
+    map_exponent(r, dx, e, [&](float d) { return c * q_of(d); });
+    for (int q = mail[threadIdx.x]; q != kNone; q = next[q])
+      put(dx + id[q], c * (q_of(e.of(xl[q])) - p[q]));
   }
 }
 
