@@ -694,8 +694,12 @@ __global__ __launch_bounds__(64) void embed_grad_kernel(
   const int cnt = static_cast<int>(n - base < size ? n - base : size);
   const int64_t col0 = static_cast<int64_t>(blockIdx.y) * (64 * VEC * P) + lane * VEC;
   bool on[P];
+  int64_t load_col[P];  // a lane behind the last column reads the first one
 #pragma unroll
-  for (int k = 0; k < P; ++k) on[k] = col0 + k * 64 * VEC < dim;
+  for (int k = 0; k < P; ++k) {
+    on[k] = col0 + k * 64 * VEC < dim;
+    load_col[k] = on[k] ? col0 + k * 64 * VEC : 0;
+  }
   uint32_t before = base > 0 ? pairs[base - 1][0] : vocab;
   float acc[P][VEC] = {};
   int slot = 0;       // where an unfinished run's sum goes: 0 while it began earlier
@@ -712,27 +716,27 @@ __global__ __launch_bounds__(64) void embed_grad_kernel(
     if (part == 0) slot = rows > 0 && __builtin_amdgcn_readlane(mine[0], 0) == before ? 0 : 1;
     const int64_t in_at = static_cast<int64_t>(mine[1]) * istride;
     const int64_t out_at = static_cast<int64_t>(mine[0]) * ostride;
+    if (rows == 0) break;
     struct Rows {
       RawVec<TI, VEC> x[kBatch][P];
-      RawVec<TO, VEC> old[ACC ? kBatch : 1][P];  // what the rows hold where a run ends
+      RawVec<TO, VEC> old[ACC ? kBatch : 1][P];  // what the table's rows hold
     } buf[2];
+    // No branches: the loads of a batch stay in flight while the last one is
+    // added.  Behind the last row it is read again, as is, with ACC, a table
+    // row for every row of its run; both from the caches.
     auto fetch = [&](int from, Rows& to) {
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int e = from + b;
-        if (e >= rows) break;
-        const TI* src = dout + lane_of(in_at, e) + col0;
+        const int e = from + b < rows ? from + b : rows - 1;
+        const TI* src = dout + lane_of(in_at, e);
 #pragma unroll
         for (int k = 0; k < P; ++k)
-          if (on[k]) to.x[b][k] = *reinterpret_cast<const RawVec<TI, VEC>*>(src + k * 64 * VEC);
+          to.x[b][k] = *reinterpret_cast<const RawVec<TI, VEC>*>(src + load_col[k]);
         if constexpr (ACC) {
-          if ((ends >> e) & 1) {
-            const TO* dst = dtable + lane_of(out_at, e) + col0;
+          const TO* dst = dtable + lane_of(out_at, e);
 #pragma unroll
-            for (int k = 0; k < P; ++k)
-              if (on[k])
-                to.old[b][k] = *reinterpret_cast<const RawVec<TO, VEC>*>(dst + k * 64 * VEC);
-          }
+          for (int k = 0; k < P; ++k)
+            to.old[b][k] = *reinterpret_cast<const RawVec<TO, VEC>*>(dst + load_col[k]);
         }
       }
     };
@@ -773,10 +777,10 @@ __global__ __launch_bounds__(64) void embed_grad_kernel(
     };
     fetch(0, buf[0]);
     for (int from = 0; from < rows; from += 2 * kBatch) {
-      if (from + kBatch < rows) fetch(from + kBatch, buf[1]);
+      fetch(from + kBatch, buf[1]);
       add(from, buf[0]);
-      if (from + 2 * kBatch < rows) fetch(from + 2 * kBatch, buf[0]);
-      if (from + kBatch < rows) add(from + kBatch, buf[1]);
+      fetch(from + 2 * kBatch, buf[0]);
+      add(from + kBatch, buf[1]);
     }
   }
   if (open) {
