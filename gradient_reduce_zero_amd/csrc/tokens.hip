@@ -1906,8 +1906,9 @@ int dp_embed_lookup(const void* table, int table_dtype, int64_t vocab, int64_t d
   if ((st = check_matrix(out, out_dtype, n, dim, out_stride)) != GRZ_OK) return st;
   if (n == 0 || dim == 0) return check_matrix(nullptr, table_dtype, 0, dim, table_stride);
   if ((st = check_matrix(table, table_dtype, vocab, dim, table_stride)) != GRZ_OK) return st;
-  if (overlap(table, span_of(table_dtype, vocab, dim, table_stride), out,
-              span_of(out_dtype, n, dim, out_stride)))
+  const size_t out_bytes = span_of(out_dtype, n, dim, out_stride);
+  if (overlap(table, span_of(table_dtype, vocab, dim, table_stride), out, out_bytes) ||
+      overlap(ids, static_cast<size_t>(n) * (id_bits / 8), out, out_bytes))
     return GRZ_EINVAL;
   if (table_dtype == GRZ_BF16)
     return out_dtype == GRZ_BF16

@@ -605,3 +605,120 @@ def test_two_streams_at_once():
     grz.dp_embed_lookup(one["table"], one["ids"], one["out"], scale=2.0, stream=streams[0])
     torch.cuda.synchronize()
     assert torch.equal(one["out"], want[0]["out"])
+
+
+# -- large sizes ---------------------------------------------------------------------------
+
+def test_rows_beyond_one_launch():
+    # The row kernels take 2^21 rows a launch, the lookup 2^23.
+    n, v = 2 ** 21 + 5, 8
+    x = logits_of(n, v, BF16)
+    t = token_ids(n, v, 70)
+    lp, h, ids, _ = logprob_call(x, t, 2)
+    tail = slice(n - 8, n)
+    sm = ref.Softmax(x[tail])
+    tc = t[tail].cpu()
+    ok = (tc >= 0) & (tc < v)
+    zero = torch.zeros(8, dtype=torch.float64)
+    at = tc.clamp(0, v - 1)[:, None]
+    ref.assert_close(lp[tail], torch.where(ok, sm.lq.gather(1, at)[:, 0], zero),
+                     torch.where(ok, sm.tol.gather(1, at)[:, 0], zero), "logprob")
+    assert torch.equal(ids[tail].cpu().long(), order_of(x[tail], 2))
+    w = torch.zeros(n, device=DEV)
+    w[0] = w[-1] = 2.0
+    dx, loss = torch.full_like(x, 5.0), torch.empty(n, device=DEV)
+    grz.dp_distill_grad(x, ids, torch.zeros(n, 2, device=DEV), dx, weights=w, loss=loss)
+    ends = torch.tensor([0, n - 1], device=DEV)
+    d = ref.Distill(x[ends], ids[ends], torch.zeros(2, 2), 1.0, w[ends])
+    ref.assert_close(dx[ends], d.dx, d.dx_tol, "dlogits")
+    ref.assert_close(loss[ends], d.loss, d.loss_tol, "loss")
+    assert (dx[1:-1] == 0).all() and (loss[1:-1] == 0).all()
+    n = 2 ** 23 + 3
+    table, _ = matrix(5, 4, BF16, seed=71)
+    ids = torch.arange(n, device=DEV, dtype=torch.int32) % 5
+    out = torch.zeros(n, 4, device=DEV, dtype=BF16)
+    grz.dp_embed_lookup(table, ids, out)
+    assert torch.equal(out, table[ids.long()])
+
+
+def test_logits_beyond_32_bit_offsets():
+    # 86000 rows of 50304: the last ones begin past 2^32 elements.
+    n, v, stride = 86000, 50257, 50304
+    x = torch.empty(n * stride, device=DEV, dtype=BF16).view(n, stride)[:, :v]
+    last = logits_of(3, v, BF16, seed=72)
+    x[-3:] = last
+    w = torch.zeros(n, device=DEV)
+    w[-3:] = 1.5
+    ids, z = teacher_of(3, v, 9, 73, 64, F32)
+    all_ids, all_z = torch.zeros(n, 9, device=DEV, dtype=torch.long), torch.zeros(n, 9, device=DEV)
+    all_ids[-3:], all_z[-3:] = ids, z
+    loss = torch.empty(n, device=DEV)
+    grz.dp_distill_grad(x, all_ids, all_z, x, temperature=2.0, weights=w, loss=loss)
+    d = ref.Distill(last, ids, z, 2.0, w[-3:])
+    ref.assert_close(x[-3:], d.dx, d.dx_tol, "dlogits")
+    ref.assert_close(loss[-3:], d.loss, d.loss_tol, "loss")
+    assert (x[:-3] == 0).all() and (loss[:-3] == 0).all()
+    x[-3:] = last
+    lp, h, top, tl = (torch.empty(n, device=DEV), torch.empty(n, device=DEV),
+                      torch.empty(n, 4, device=DEV, dtype=torch.int32),
+                      torch.empty(n, 4, device=DEV))
+    grz.dp_token_logprobs(x, None, None, h, top, tl)
+    sm = ref.Softmax(last)
+    want, tol = sm.entropy()
+    ref.assert_close(h[-3:], want, tol, "entropy")
+    order = order_of(last, 4)
+    assert torch.equal(top[-3:].cpu().long(), order)
+    assert (top[:-3] == torch.arange(4, device=DEV, dtype=torch.int32)).all()
+
+
+# -- refusals that need device tensors ---------------------------------------------------------
+
+def test_binding_refuses_layouts_types_and_shapes():
+    f = torch.zeros(6, 8, device=DEV)
+    i = torch.zeros(6, device=DEV, dtype=torch.long)
+    col = torch.zeros(6, device=DEV)
+    ws = torch.zeros(1 << 16, device=DEV, dtype=torch.uint8)
+    bad = [
+        (ValueError, lambda: grz.dp_embed_lookup(f.t(), i, f)),              # columns not adjacent
+        (ValueError, lambda: grz.dp_embed_lookup(f, i, f[:1].expand(6, 8))),  # rows overlap
+        (ValueError, lambda: grz.dp_embed_lookup(f, i[:5], f.clone())),
+        (ValueError, lambda: grz.dp_embed_lookup(f, i, torch.zeros(6, 7, device=DEV))),
+        (TypeError, lambda: grz.dp_embed_lookup(f, i.float(), f.clone())),
+        (TypeError, lambda: grz.dp_embed_lookup(f.half(), i, f)),
+        (ValueError, lambda: grz.dp_embed_lookup(f.view(-1), i, f)),
+        (ValueError, lambda: grz.dp_embed_lookup(f, torch.zeros(12, device=DEV,
+                                                                dtype=torch.long)[::2],
+                                                 f.clone())),
+        (grz.GrzError, lambda: grz.dp_embed_lookup(f, i, f)),                 # over its table
+        (ValueError, lambda: grz.dp_embed_grad(f, i, f.clone(), None)),
+        (ValueError, lambda: grz.dp_embed_grad(f, i, f.clone(), ws[:8])),
+        (grz.GrzError, lambda: grz.dp_embed_grad(f, i, f.clone(), ws[4:])),
+        (grz.GrzError, lambda: grz.dp_embed_grad(f, i, f, ws)),
+        (TypeError, lambda: grz.dp_token_logprobs(f, i, logprob=col.double())),
+        (ValueError, lambda: grz.dp_token_logprobs(f, i, logprob=col[:5])),
+        (ValueError, lambda: grz.dp_token_logprobs(f, i, top_ids=i.int())),
+        (ValueError, lambda: grz.dp_token_logprobs(
+            f, i, top_ids=torch.zeros(6, 2, device=DEV, dtype=torch.int32))),
+        (grz.GrzError, lambda: grz.dp_token_logprobs(
+            f, top_ids=torch.zeros(6, 9, device=DEV, dtype=torch.int32),
+            top_logprobs=torch.zeros(6, 9, device=DEV))),
+        (grz.GrzError, lambda: grz.dp_token_logprobs(f, i)),
+        (grz.GrzError, lambda: grz.dp_token_logprobs(f, logprob=col)),
+        (TypeError, lambda: grz.dp_token_logprobs_grad(f, i, col, None, f.bfloat16())),
+        (ValueError, lambda: grz.dp_token_logprobs_grad(f, i, col, None, f[:5])),
+        (grz.GrzError, lambda: grz.dp_token_logprobs_grad(f, i, None, None, f.clone())),
+        (ValueError, lambda: grz.dp_distill_loss(f, i, f, col)),
+        (ValueError, lambda: grz.dp_distill_loss(f, i[:, None], f, col)),
+        (grz.GrzError, lambda: grz.dp_distill_loss(f, i[:, None], f[:, :1].contiguous(), col,
+                                                   temperature=0.0)),
+        (grz.GrzError, lambda: grz.dp_distill_grad(f[:, :4], i[:, None],
+                                                   f[:, :1].contiguous(), f[:, 2:6])),
+        (ValueError, lambda: grz.dp_distill_grad(f, i[:, None], f[:, :1].contiguous(),
+                                                 torch.zeros(6, 8))),
+    ]
+    for k, (error, call) in enumerate(bad):
+        with pytest.raises(error):
+            call()
+            raise AssertionError(f"call {k} was not refused")
+    torch.cuda.synchronize()
+    assert (f == 0).all()
