@@ -1152,6 +1152,7 @@ __device__ __forceinline__ void wave_fence() {
 
 constexpr int kCandidates = 512;
 constexpr int kGroups = 256, kFewGroups = 64;
+constexpr int kAllListed = 128;  // a vocabulary whose every element is a candidate
 constexpr int kHolders = 16;     // lanes of a wave whose elements are searched at once
 
 template <int NT, int NV> struct TopLds {
@@ -1248,9 +1249,13 @@ __device__ __forceinline__ void top_list(const Row<T, NT, NV, ONCE>& r, int voca
                                          bool exact, int top, TopLds<NT, NV>& lds, F emit) {
   constexpr int E = Row<T, NT, NV, ONCE>::E;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (exact && top <= TopLds<NT, NV>::G) {
+  const bool every = NT == 64 && vocab <= kAllListed;
+  if (every || (exact && top <= TopLds<NT, NV>::G)) {
     const float bound = lds.bound;
-    if constexpr (NV > 0) {
+    if (every) {
+      if (lane == 0) lds.count = static_cast<uint32_t>(vocab);
+      r.each([&](float x, int index) { lds.found[index] = order_of(x, index); });
+    } else if constexpr (NV > 0) {
       bool holds = own_max >= bound;
       for (uint64_t mask = __ballot(holds); mask != 0; mask = __ballot(holds)) {
         const int mine = __popcll(mask & ((1ull << lane) - 1));
@@ -1276,7 +1281,7 @@ __device__ __forceinline__ void top_list(const Row<T, NT, NV, ONCE>& r, int voca
     } else {
       r.vectors([&](float (&x)[E], int at) { add_candidates(x, at, bound, lds); });
     }
-    if (r.edge >= 0) {
+    if (!every && r.edge >= 0) {
       const float x[1] = {r.edge_x};
       add_candidates(x, r.edge, bound, lds);
     }
@@ -1284,11 +1289,10 @@ __device__ __forceinline__ void top_list(const Row<T, NT, NV, ONCE>& r, int voca
     const int count = static_cast<int>(lds.count);
     if (count <= kCandidates) {
       // `parts` neighbouring lanes share a candidate's comparisons.
-      int parts = 1;
-      while (parts < 8 && parts * 2 * count <= NT) parts *= 2;
-      const int each = NT / parts, part = threadIdx.x % parts;
-      for (int c0 = 0; c0 + wave * 64 / parts < count; c0 += each) {
-        const int c = c0 + static_cast<int>(threadIdx.x) / parts;
+      for (int c0 = 0, parts; c0 < count; c0 += NT / parts) {
+        for (parts = 1; parts < 8 && parts * 2 * (count - c0) <= NT;) parts *= 2;
+        if (c0 + wave * 64 / parts >= count) break;
+        const int c = c0 + static_cast<int>(threadIdx.x) / parts, part = threadIdx.x % parts;
         const uint64_t mine = c < count ? lds.found[c] : ~0ull;
         int place = 0;
 #pragma unroll 4
@@ -1361,7 +1365,8 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void logprob_kernel(LogprobArgs
   if (!GRAD && a.top > 0) top_groups(own_max, lds_top);
   const Exponent e(block_max<NT>(own_max, lds_max), 1.0f);
   if (NT == 64) __syncthreads();
-  if (!GRAD && a.top > 0 && threadIdx.x >= NT - 64) top_bound(a.top, lds_top);
+  if (!GRAD && a.top > 0 && threadIdx.x >= NT - 64 && (NT > 64 || a.vocab > kAllListed))
+    top_bound(a.top, lds_top);
   float sum[2] = {0.0f, 0.0f};
   each_exponent(r, e, [&](float d) {
     const float p = __builtin_amdgcn_exp2f(d);
