@@ -177,6 +177,12 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int id_bits, int64_t i
                        : static_cast<int64_t>(static_cast<const int32_t*>(ids)[i]);
 }
 
+// What waves read of each other's LDS writes without a barrier is their own.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // ---------------------------------------------------------------------------
 // Lookup: one wave per row, its lanes along the columns.
 
@@ -870,6 +876,81 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(
   }
 }
 
+// Small tables and few ids, in one launch and without a sort: a workgroup per
+// (table row, column piece) reads all ids; each wave collects the positions of
+// its share that name the row, in order, and sums their rows, then the waves'
+// sums are added in order.  2048 ids x 384 into 65 rows: 7.4 us a call against
+// 13.2 us for sort, sum and join, whose three launches are three latencies; 4096
+// x 256 into 512 rows 8.3 against 14.1 us.  One workgroup's waves sum all of a
+// row, so few rows for many ids take the sort (4096 x 1600 into 8 rows: 34
+// against 19 us).
+constexpr int kDirectWaves = 16;
+constexpr int64_t kDirectIds = 4096, kDirectGroups = 512, kDirectMean = 32;
+
+template <typename TI, typename TO, int VEC, bool ACC>
+__global__ __launch_bounds__(kDirectWaves * 64) void direct_grad_kernel(
+    const TI* __restrict__ dout, int64_t istride, const void* __restrict__ ids, int id_bits, int n,
+    int64_t dim, float scale, TO* __restrict__ dtable, int64_t ostride) {
+  constexpr int kShare = kDirectIds / kDirectWaves, kFetch = 8;
+  __shared__ uint16_t list[kDirectWaves][kShare];
+  __shared__ float part[kDirectWaves][64 * VEC];
+  __shared__ int found[kDirectWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = blockIdx.x;
+  const int share = (n + kDirectWaves * 64 - 1) / (kDirectWaves * 64) * 64;
+  int count = 0;
+#pragma unroll
+  for (int k = 0; k < kShare / 64; ++k) {
+    const int i = wave * share + k * 64 + lane;
+    const bool mine = k * 64 < share && i < n && id_at(ids, id_bits, i) == row;
+    const uint64_t mask = __ballot(mine);
+    if (mine) list[wave][count + __popcll(mask & ((1ull << lane) - 1))] = static_cast<uint16_t>(i);
+    count += __popcll(mask);
+  }
+  if (lane == 0) found[wave] = count;
+  wave_fence();
+  const int64_t col = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * VEC;
+  const bool on = col < dim;
+  const int64_t load_col = on ? col : 0;
+  float acc[VEC] = {};
+  for (int from = 0; from < count; from += kFetch) {
+    RawVec<TI, VEC> x[kFetch];
+#pragma unroll
+    for (int b = 0; b < kFetch; ++b) {  // behind the last one it is read again
+      const int e = from + b < count ? from + b : count - 1;
+      const int at = __builtin_amdgcn_readfirstlane(list[wave][e]);
+      x[b] = load_raw<false, TI, VEC>(dout + at * istride + load_col);
+    }
+#pragma unroll
+    for (int b = 0; b < kFetch; ++b) {
+      if (from + b >= count) break;
+      float y[VEC];
+      widen_vec<TI, VEC>(x[b], y);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] += y[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) part[wave][lane * VEC + i] = acc[i];
+  __syncthreads();
+  if (wave != 0 || !on) return;
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kDirectWaves; ++w) total += found[w];
+  if (ACC && total == 0) return;  // a row that no id names is not touched
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    acc[i] = part[0][lane * VEC + i];
+#pragma unroll
+    for (int w = 1; w < kDirectWaves; ++w) acc[i] += part[w][lane * VEC + i];
+  }
+  TO* dst = dtable + row * ostride + col;
+  RawVec<TO, VEC> old{};
+  if (ACC) old = load_raw<false, TO, VEC>(dst);
+  finish_row<ACC, TO, VEC>(dst, acc, scale, old);
+}
+
 // ---------------------------------------------------------------------------
 // Rows over the vocabulary.  One workgroup of NT threads per row.  The row is
 // read as 16-byte vectors from its first 16-byte border on; the elements
@@ -1129,12 +1210,6 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
-// What waves read of each other's LDS writes without a barrier is their own.
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // The top list.  The largest elements of G groups of threads are found first:
 // the top-th largest of those bounds the list from below, and few elements lie
 // at or above it.  They are gathered and each finds its place by counting the
@@ -1147,7 +1222,7 @@ __device__ __forceinline__ void wave_fence() {
 // So the bound is found by the last wave beside the others' exponentials, and
 // the gathering needs no barrier of its own: few lanes hold candidates, and a
 // wave's put what they hold into its own LDS, where every lane searches a vector
-// of it.  Measured at 4096 x 50257, 64 places: XX us, YY us without the list, 114 us
+// of it.  Measured at 4096 x 50257, 64 places: 97 us, 67 us without the list, 114 us
 // with each step behind a barrier and each thread searching its own elements.
 
 constexpr int kCandidates = 512;
@@ -1590,7 +1665,12 @@ int row_launch(void (*kernel)(Args), int threads, size_t lds, Args a, int64_t n,
   return GRZ_OK;
 }
 
-// Threads per row and kept vectors per thread, by the row's 16-byte vectors.
+// Threads per row and kept vectors per thread, by the row's 16-byte vectors: as
+// many threads as leave each about eight vectors, all on their way at once, so
+// that two workgroups of 1024 (or four of 512, ...) share a CU.  The gradient of
+// 4096 x 50257 logits: 154 us with 1024 threads of 8 vectors, 162 with 512 of 13
+// (three workgroups on a CU), 174 with 256 of 25 (four).  One wave per row up to
+// 256 vectors (its lists are at most 64 long).
 #define GRZ_ROW_SHAPES(CALL)                                  \
   const int64_t vectors = a.vocab / (16 / (int)sizeof(T));    \
   if (vectors <= 64 * 4 && a.top <= 64) return CALL(64, 4);   \
@@ -1837,6 +1917,13 @@ int embed_grad_launch(const TI* dout, int64_t istride, const void* ids, int id_b
     const ZeroRows z = zero_part(dtable, ostride, vocab, dim, 0, 1, true);
     return launch(zero_rows_kernel, dim3(zero_blocks(z, 4)), dim3(256), stream, z);
   }
+  const int64_t pieces = ceil_div(dim, 64 * VEC);
+  if (n <= kDirectIds && n <= kDirectMean * vocab && vocab * pieces <= kDirectGroups)
+    return launch(accumulate ? direct_grad_kernel<TI, TO, VEC, true>
+                             : direct_grad_kernel<TI, TO, VEC, false>,
+                  dim3(static_cast<unsigned>(vocab), static_cast<unsigned>(pieces)),
+                  dim3(kDirectWaves * 64), stream, dout, istride, ids, id_bits,
+                  static_cast<int>(n), dim, scale, dtable, ostride);
   const GradPlan p = grad_plan(n, vocab, dim);
   u32x2* const pairs[2] = {reinterpret_cast<u32x2*>(ws),
                            reinterpret_cast<u32x2*>(ws + p.pairs_b)};
@@ -1856,7 +1943,6 @@ int embed_grad_launch(const TI* dout, int64_t istride, const void* ids, int id_b
                : sort_launch<kLittleSort>(src, n, p, pairs, counts, totals, zeros, &sorted,
                                           stream);
   if (st != GRZ_OK) return st;
-  const int64_t pieces = ceil_div(dim, 64 * VEC);
   int64_t waves = 0;
   auto kernel = accumulate ? grad_kernel_for<TI, TO, VEC, true>(pieces, &waves)
                            : grad_kernel_for<TI, TO, VEC, false>(pieces, &waves);

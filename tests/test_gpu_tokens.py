@@ -164,6 +164,31 @@ def test_embed_grad_of_many_ids(n, vocab):
     ref.assert_close(table, want, tol, "dtable")
 
 
+@pytest.mark.parametrize("n,vocab,dim", [(2080, 65, 384), (2081, 65, 384), (4096, 128, 1024),
+                                         (4096, 128, 1028), (4097, 300, 8), (513, 17, 63),
+                                         (64, 2, 5), (65, 2, 5), (4095, 512, 256)])
+@pytest.mark.parametrize("ti,to", [(BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad_of_small_tables(n, vocab, dim, ti, to, accumulate):
+    # On both sides of where a small table is summed without a sort; rows that no
+    # id names, one that half of them name.
+    ids = token_ids(n, vocab, 17)
+    ids[: n // 2] = vocab - 1
+    ids[ids == 1] = 0
+    dout, _ = matrix(n, dim, ti, seed=18)
+    table, buf = matrix(vocab, dim, to, seed=19, pad=3, shift=1)
+    before, old = buf.clone(), table.clone()
+    grad_call(dout, ids, table, scale=1.25, accumulate=accumulate)
+    want, tol = ref.embed_grad(dout, ids, vocab, 1.25, old if accumulate else None)
+    ref.assert_close(table, want, tol, "dtable")
+    assert outside_untouched(table, buf, before)
+    if accumulate:
+        assert torch.equal(table[1].view(torch.uint8), old[1].view(torch.uint8))
+    again = old.clone()
+    grad_call(dout, ids, again, scale=1.25, accumulate=accumulate)
+    ref.assert_close(again, want, tol, "another layout")
+
+
 def test_embed_grad_bits_do_not_change_and_follow_the_rows():
     n, vocab, dim = 20011, 1000, 64
     dout, _ = matrix(n, dim, BF16, seed=10)
