@@ -26,9 +26,12 @@ _TYPES = {torch.float32: N.GRZ_F32, torch.bfloat16: N.GRZ_BF16}
 _IDS = {torch.int32: 32, torch.int64: 64}
 _F32, _I32 = torch.float32, torch.int32
 
-# The smallest calls take a few microseconds on the device, so the checks below
-# keep to the cheapest accessors: device indices (-1 for the host) instead of
-# device objects, and messages only where a check has failed.
+# The smallest calls take a few microseconds on the device, about what the host
+# needs for one launch, so the checks below use the cheapest accessors: device
+# indices (-1 for the host) instead of device objects, and explanations only
+# where a check has failed.
+_current_gpu = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _device(t, name, dev=None):
@@ -47,14 +50,15 @@ def _rows(t, name, dev, rows=None, cols=None, dtype=None):
     """(pointer, type, rows, columns, row stride) of a row matrix on GPU ``dev``."""
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         _device(t, name, dev)
-    kind = _TYPES.get(t.dtype)
-    if kind is None or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype or 'float32 or bfloat16'}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected two dimensions")
-    r, c = t.shape
+    shape, own = t.shape, t.dtype
+    kind = _TYPES.get(own)
+    if kind is None or (dtype is not None and own != dtype):
+        raise TypeError(f"{name} has dtype {own}, expected {dtype or 'float32 or bfloat16'}")
+    if len(shape) != 2:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected two dimensions")
+    r, c = shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected "
                          f"({'any' if rows is None else rows}, {'any' if cols is None else cols})")
     stride, inner = t.stride()
     if inner != 1 and c > 1:
@@ -85,23 +89,24 @@ def _ids(t, name, dev, *shape):
     """(pointer, bits) of a contiguous id array."""
     if t is None:
         return None, 32
-    bits = _IDS.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    own = t.dtype if isinstance(t, torch.Tensor) else None
+    bits = _IDS.get(own)
     if bits is None:
         raise TypeError(f"{name} must be an int32 or int64 tensor")
-    return _list(t, name, dev, t.dtype, *shape), bits
+    return _list(t, name, dev, own, *shape), bits
 
 
 def _call(name, dev, stream, *args):
     """Call entry point ``name`` with GPU ``dev`` current, on ``stream`` or its
     current stream."""
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev)
+        handle = _current_stream(dev)
     elif stream.device.index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
     else:
         handle = stream.cuda_stream
     fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev:
+    if _current_gpu() == dev:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
