@@ -30,12 +30,13 @@ constexpr int64_t kMaxRows = INT32_MAX;  // rows and columns of one call
 constexpr int64_t kGradIds = int64_t{1} << 28, kGradRows = int64_t{1} << 26;
 constexpr int64_t kGradCols = int64_t{65535} * 64;
 constexpr int64_t kRowBatch = int64_t{1} << 21;  // rows of one launch of the row kernels
+constexpr float kMinTemperature = 1e-18f, kMaxTemperature = 1e18f;
 
 template <typename T> struct NoDeduce { using type = T; };
 
 // Returns the status of this launch alone (hipLaunchKernel's return value).  A
-// dispatch counts its threads in 32 bits; the entry points' limits and
-// row_batches keep below that.
+// dispatch counts its threads in 32 bits; the entry points' limits and kRowBatch
+// keep below that.
 template <typename... A>
 int launch_lds(void (*kernel)(A...), size_t lds, dim3 grid, dim3 block, hipStream_t stream,
                typename NoDeduce<A>::type... a) {
@@ -184,7 +185,10 @@ __device__ __forceinline__ void wave_fence() {
 }
 
 // ---------------------------------------------------------------------------
-// Lookup: one wave per row, its lanes along the columns.
+// Lookup: one wave per row, its lanes along the columns, four 16-byte accesses
+// of each on their way.  Bound by HBM: 16384 rows of 4096 bf16 out of 32000 in
+// 32 us, 6.6 TB/s of 77 MB read (frequent rows once per XCD's L2) and 134 MB
+// written; with two accesses on their way and plain stores 46 us.
 
 template <typename TI, typename TO, int VEC>
 __global__ __launch_bounds__(256) void lookup_kernel(const TI* __restrict__ table, int64_t tstride,
@@ -224,17 +228,21 @@ __global__ __launch_bounds__(256) void lookup_kernel(const TI* __restrict__ tabl
 // every row.  What a sort costs here is its launches' latency, so few of them:
 //
 //  - up to kRankIds ids one launch: an id's place is the number of ids before
-//    it in the sorted order, counted by comparing it with all of them;
+//    it in the sorted order, counted by comparing it with all of them (2048
+//    ids: 4.3 us; the arithmetic grows with n^2: at 16384 ids the gradient then
+//    takes 51-56 us against 38 us with the next one);
 //  - up to kMergeIds two: tiles of kMergeTile ids are sorted by that count,
 //    then an id's place is the sum of its places in all tiles, each found by a
-//    binary search in LDS;
+//    binary search in LDS (8011 ids: 5 + 6 us, against 22 us for the radix
+//    sort's four launches);
 //  - beyond that a radix sort, least significant digit first, of a count and a
 //    scatter per pass; a workgroup of NT threads takes a tile of NT *
 //    kSortItems pairs: 1024 up to kSmallSort ids, so that they still spread
-//    over many CUs, 4096 beyond.
+//    over many CUs, 4096 beyond (1 M ids: 5 + 5 + 13 us a pass).
 //
 // The sort leaves HBM idle, so the launches that place pairs carry workgroups
-// behind their own that write the table's zeros.
+// behind their own that write the table's zeros (16384 ids, 77 MB of zeros: 19 us
+// for both against 10 + 11 us one after the other).
 
 constexpr int kRankIds = 4096;
 constexpr int kRankWaves = 16;
@@ -381,6 +389,7 @@ __device__ __forceinline__ void tile_ranks(const u32x2 (&pair)[kSortItems], int6
   const int digits = 1 << bits;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int d = lane; d < digits; d += 64) lds.before[wave][d] = 0;
+  wave_fence();
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
     const bool in = (wave * kSortItems + j) * 64 + lane < left;
@@ -393,9 +402,11 @@ __device__ __forceinline__ void tile_ranks(const u32x2 (&pair)[kSortItems], int6
     const uint32_t earlier = static_cast<uint32_t>(__popcll(same & ((1ull << lane) - 1)));
     uint32_t r = 0;
     if (in) r = lds.before[wave][d];
+    wave_fence();
     if (in && earlier == 0)
       lds.before[wave][d] = static_cast<uint16_t>(r + static_cast<uint32_t>(__popcll(same)));
     rank[j] = r + earlier;
+    wave_fence();
   }
   __syncthreads();
 #pragma unroll
@@ -582,6 +593,7 @@ __global__ __launch_bounds__(kRankWaves * 64) void merge_tiles_kernel(
 // pairs in all and in the tiles before comes, with few tiles, straight from
 // counts[tile][digit], and with more from sort_scan_kernel's results.
 constexpr int kDirectTiles = 64;
+static_assert(kSmallSort <= int64_t{kDirectTiles} * tile_of(kLittleSort), "little tiles");
 
 template <int NT, bool SCANNED>
 __global__ __launch_bounds__(NT) void sort_scatter_kernel(
@@ -646,7 +658,9 @@ __global__ __launch_bounds__(NT) void sort_scatter_kernel(
 //
 // A wave's columns are P pieces of 64 * VEC, so that what it does per row (its
 // address, where runs end) is shared by up to 2 KB of it; the next kBatch rows
-// are on their way while the last ones are added.
+// are on their way while the last ones are added.  Bound by HBM for many rows (1 M
+// of 768 bf16: 1.6 GB in 300 us), by the chain pairs - rows - stores for few
+// (16384: 25 MB in 10 us).
 //
 // Rows are loaded and written, and zeros written, non-temporally, except where
 // the table's rows are added to (its loads then measured 6 % slower) and beside
@@ -817,7 +831,9 @@ __global__ __launch_bounds__(64) void embed_grad_kernel(
 
 // One workgroup per (chunk border, column block); the border where a run first
 // crosses adds the whole run: its waves take equal parts of the run's partial
-// sums, in order, then the waves' sums in order.
+// sums, in order, then the waves' sums in order.  Most borders have nothing to add
+// and leave after one read, so more waves cost more than they gain: 16384 ids 6 us;
+// with 16 waves the fp32 gradient of 8011 x 1600 takes 39 us instead of 33.
 constexpr int kJoinWaves = 4;
 
 template <typename TO, int VEC, bool ACC>
@@ -960,7 +976,7 @@ __global__ __launch_bounds__(kDirectWaves * 64) void direct_grad_kernel(
 // NV > 0: the row is read once and kept in registers, up to NV vectors per
 // thread, so that its maximum, its sums and its gradient cost one pass over
 // HBM.  NV = 0, for rows too long for that: each step reads the row again.
-
+//
 // ONCE: nothing reads the row again after this load (non-temporal).
 
 template <typename T, int NT, int NV, bool ONCE = false> struct Row {
@@ -1160,14 +1176,15 @@ __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* lds) {
 constexpr int kept_waves(int nv) { return nv > 8 ? 4 : 8; }
 
 // The row's exponents, in powers of two: an element's is x * l2 - at, l2 =
-// log2(e) / T, with one fused rounding.  `at` = max * l2, rounded, cancels from
-// everything normalised by the sum.  Where max * l2 could overflow (logits at
-// the type's lowest value) the difference is formed first.
+// log2(e) / T, with one fused rounding.  `at` = max * l2, rounded (by at most
+// 1/16), cancels from everything normalised by the sum.  Where max * l2 is so
+// large that its rounding would shift the exponents out of range (huge logits,
+// masks of the type's lowest value) the difference is formed first.
 struct Exponent {
   float inv_tau, l2, max, at;
   bool plain;
   __device__ __forceinline__ Exponent(float m, float inv)
-      : inv_tau(inv), l2(kLog2e * inv), max(m), at(m * l2), plain(fabsf(at) < 1.0e30f) {}
+      : inv_tau(inv), l2(kLog2e * inv), max(m), at(m * l2), plain(fabsf(at) < 1.0e6f) {}
   __device__ __forceinline__ float far(float x) const { return (x - max) * l2; }
   __device__ __forceinline__ float near(float x) const { return fmaf(x, l2, -at); }
   __device__ __forceinline__ float of(float x) const { return plain ? near(x) : far(x); }
@@ -1412,6 +1429,10 @@ template <typename T> struct LogprobArgs {
 
 // With d the elements' exponents, S = sum 2^d and A = sum 2^d d:
 // log2 q = d - log2 S, H = (log2 S - A / S) ln 2.
+//
+// Bound by HBM: 4096 x 50257 bf16 in 67 us (6.1 TB/s), its gradient in 154 us, that
+// of 8192 x 32000 in 183 us (5.7 TB/s, reads and writes mixed); one workgroup of 256
+// threads reading the row for each step took 307-315 us for such gradients.
 template <typename T, int NT, int NV, bool GRAD>
 __global__ __launch_bounds__(NT, kept_waves(NV)) void logprob_kernel(LogprobArgs<T> a) {
   __shared__ float lds_max[NT / 64];
@@ -1508,7 +1529,8 @@ template <typename T> struct DistillArgs {
 // the row's, so that the list is ready when the row comes.  A listed element's
 // gradient is stored by the thread that holds it, over what it has stored
 // before: a thread finds its entries through `mail`, and no wave has to wait for
-// another's stores.
+// another's stores (4096 x 50257 bf16, 32 listed: 151 us, 5.5 TB/s, against 167 us
+// with the list read behind the row and its elements stored behind a barrier).
 template <typename T, int NT, int NV, bool GRAD>
 __global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs<T> a) {
   constexpr int M = GRZ_MAX_TOP / 64, kNone = 255;
@@ -1740,8 +1762,8 @@ int distill_entry(const void* logits, int dtype, int64_t n, int64_t vocab, int64
   int st = check_matrix(logits, dtype, n, vocab, stride);
   if (st != GRZ_OK) return st;
   if (k < 1 || k > GRZ_MAX_TOP || !float_type(teacher_dtype)) return GRZ_EINVAL;
-  if (!(temperature > 0.0f) || !(temperature < INFINITY) || !(1.0f / temperature < INFINITY))
-    return GRZ_EINVAL;
+  // T^2 and log2(e) / T stay finite.
+  if (!(temperature >= kMinTemperature) || !(temperature <= kMaxTemperature)) return GRZ_EINVAL;
   if (n > kMaxRows / k) return GRZ_ERANGE;
   if ((st = check_ids(ids, id_bits, n * k)) != GRZ_OK) return st;
   if (n == 0) return GRZ_OK;
@@ -1783,8 +1805,9 @@ struct GradPlan {
 size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 // Pairs per chunk, a power of two from 8 to 128: short chunks give few rows
-// enough waves (some 2560 of them, a column piece each), long ones keep the
-// partial sums of long runs few.
+// enough waves (a 2560th of the rows' pieces of 256 columns), long ones keep the
+// partial sums of long runs few.  16384 x 768: 34.7 us with 16, 36.8 with 8; 4096 x
+// 768: 22.4 with 8, 24.4 with 16; 16384 x 4096: 93 with 64, 102 with 16.
 int chunk_of(int64_t n, int64_t dim) {
   const int64_t want = n * ceil_div(dim, 256) / 2560;
   int c = 8;
@@ -1873,16 +1896,17 @@ int sort_launch(SortSrc src, int64_t n, const GradPlan& p, u32x2* const (&pairs)
     u32x2* out = pairs[k & 1];
     int st = launch(sort_count_kernel<NT>, dim3(tiles), threads, stream, src, n, shift, p.bits,
                     counts);
-    if (st == GRZ_OK && p.tiles <= kDirectTiles) {
-      st = launch(sort_scatter_kernel<NT, false>, grid, threads, stream, src, n, shift, p.bits,
-                  counts, totals, out, z);
-    } else if (st == GRZ_OK) {
-      st = launch(sort_scan_kernel, dim3(static_cast<unsigned>(ceil_div(digits, 64))),
-                  dim3(kScanWaves * 64), stream, counts, totals, p.tiles, digits);
-      if (st == GRZ_OK)
-        st = launch(sort_scatter_kernel<NT, true>, grid, threads, stream, src, n, shift, p.bits,
-                    counts, totals, out, z);
+    if (st != GRZ_OK) return st;
+    auto scatter = sort_scatter_kernel<NT, false>;
+    if constexpr (NT == kBigSort) {  // the little tiles are kDirectTiles at most
+      if (p.tiles > kDirectTiles) {
+        st = launch(sort_scan_kernel, dim3(static_cast<unsigned>(ceil_div(digits, 64))),
+                    dim3(kScanWaves * 64), stream, counts, totals, p.tiles, digits);
+        if (st != GRZ_OK) return st;
+        scatter = sort_scatter_kernel<NT, true>;
+      }
     }
+    st = launch(scatter, grid, threads, stream, src, n, shift, p.bits, counts, totals, out, z);
     if (st != GRZ_OK) return st;
     *sorted = out;
     src = SortSrc{nullptr, 0, out, src.vocab};
@@ -2060,6 +2084,7 @@ int dp_embed_grad(const void* dout, int dout_dtype, int64_t dout_stride, const v
   if (overlap(dout, span_of(dout_dtype, n, dim, dout_stride), dtable, table_bytes) ||
       overlap(workspace, need, dtable, table_bytes) ||
       overlap(workspace, need, dout, span_of(dout_dtype, n, dim, dout_stride)) ||
+      overlap(workspace, need, ids, static_cast<size_t>(n) * (id_bits / 8)) ||
       overlap(ids, static_cast<size_t>(n) * (id_bits / 8), dtable, table_bytes))
     return GRZ_EINVAL;
   const int acc = flags & GRZ_ACCUMULATE ? 1 : 0;

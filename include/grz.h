@@ -672,7 +672,7 @@ int dp_token_logprobs_grad(const void* logits, int dtype, int64_t n, int64_t voc
  * teacher_logits  device, n * k values of teacher_dtype (GRZ_F32 or GRZ_BF16),
  *                 contiguous; log probabilities will do.
  * k               1..GRZ_MAX_TOP.
- * temperature     T > 0, finite (and 1 / T finite).
+ * temperature     T, from 1e-18 to 1e18.
  * weights         device fp32[n], or NULL for 1.  A row of weight 0, or with
  *                 nothing listed, has loss 0 and gradient 0 whatever its
  *                 logits hold.

@@ -308,6 +308,24 @@ def test_logprobs_of_ties_and_masks(v, dtype):
 
 @pytest.mark.parametrize("v", [65, 3000, 33000])
 @pytest.mark.parametrize("dtype", [BF16, F32])
+def test_logprobs_of_huge_logits(v, dtype):
+    # Rows far from zero, whose differences are few steps of the type or none.
+    x = logits_of(8, v, dtype)
+    for i, at in enumerate((3e4, 6e5, 7e5, -8e5, 1e8, -1e10, 1e20, 3e37)):
+        x[i] = at * (1 + torch.randint(0, 3, (v,), device=DEV, generator=gen(i)) *
+                     torch.finfo(dtype).eps)
+    targets = torch.arange(8, device=DEV)
+    check_logprobs(x, targets, 5, "huge")
+    glp = torch.linspace(-1, 1, 8, device=DEV)
+    gent = torch.linspace(0.5, -0.5, 8, device=DEV)
+    dx = torch.empty_like(x)
+    grz.dp_token_logprobs_grad(x, targets, glp, gent, dx)
+    want, tol = ref.logprob_grad(x, targets, glp, gent)
+    ref.assert_close(dx, want, tol, "dlogits")
+
+
+@pytest.mark.parametrize("v", [65, 3000, 33000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_logprobs_of_rows_without_a_softmax(v, dtype):
     x = logits_of(4, v, dtype)
     x[0].fill_(-math.inf)
@@ -505,6 +523,26 @@ def test_distill_of_masked_lists_rows_and_weights(v, dtype):
     l2, g2 = torch.empty(1, device=DEV), torch.empty_like(x2)
     grz.dp_distill_grad(x2, i2, torch.zeros(1, 2, device=DEV), g2, loss=l2)
     assert l2.item() == math.inf and g2[0, 5].item() == -0.5 and torch.isfinite(g2).all()
+
+
+@pytest.mark.parametrize("tau", [1e-18, 1e-6, 1e6, 1e18])
+def test_distill_at_extreme_temperatures(tau):
+    # Cold: all of p and q on one token; hot: both uniform, p over the list.
+    n, v, k = 3, 300, 4
+    x = logits_of(n, v, F32)
+    ids, _ = teacher_of(n, v, k, 38, 64, F32)
+    z = x.gather(1, ids).contiguous()
+    z[:, 0] += 100.0
+    x[0, ids[0, 0]] = 200.0
+    loss, dx = torch.empty(n, device=DEV), torch.empty_like(x)
+    grz.dp_distill_grad(x, ids, z, dx, temperature=tau, loss=loss)
+    t = torch.tensor(tau, dtype=F32).double().item()
+    q = torch.softmax(x.double() / t, 1)
+    p = torch.zeros_like(q).scatter_add_(1, ids, torch.softmax(z.double() / t, 1))
+    assert torch.isfinite(dx).all() and not torch.isnan(loss).any()
+    # a softmax's value is off by at most a few u (1 + |x| / T) of itself; here it is 0, 1 or
+    # uniform up to 300 / T, so an absolute bound of 1e-4 T holds with room
+    assert ((dx.double() - t * (q - p)).abs() <= 1e-4 * t).all()
 
 
 def test_distill_with_one_token_is_the_cross_entropy():

@@ -75,6 +75,8 @@ def test_outputs_that_overlap_an_input_are_refused():
     assert grad(ws=C + 16) == N.GRZ_EINVAL
     assert grad(ws=A + 16) == N.GRZ_EINVAL
     assert grad(ids=C + 16) == N.GRZ_EINVAL
+    assert grad(ids=W + 16) == N.GRZ_EINVAL
+    assert lookup(ids=C + 16) == N.GRZ_EINVAL
     assert logprobs_grad(dx=A + 2) == N.GRZ_EINVAL
     assert logprobs_grad(dx=A, ds=12) == N.GRZ_EINVAL
     assert distill(dx=A + 2, which="grad") == N.GRZ_EINVAL
@@ -114,7 +116,7 @@ def test_logprobs_arguments():
 
 
 def test_distill_arguments():
-    for tau in (0.0, -1.0, float("inf"), float("nan"), 1e-45):
+    for tau in (0.0, -1.0, float("inf"), float("nan"), 1e-45, 0.9e-18, 1.1e18):
         assert distill(tau=tau) == N.GRZ_EINVAL
     assert distill(k=0) == N.GRZ_EINVAL and distill(k=N.GRZ_MAX_TOP + 1) == N.GRZ_EINVAL
     assert distill(ids=None) == N.GRZ_EINVAL and distill(z=None) == N.GRZ_EINVAL
