@@ -229,11 +229,12 @@ __global__ __launch_bounds__(256) void lookup_kernel(const TI* __restrict__ tabl
 //
 //  - up to kRankIds ids one launch: an id's place is the number of ids before
 //    it in the sorted order, counted by comparing it with all of them (2048
-//    ids: 4.3 us; the arithmetic grows with n^2: at 16384 ids the gradient then
-//    takes 51-56 us against 38 us with the next one);
+//    ids: 4.3 us; the arithmetic grows with n^2: the gradient of 4000 ids takes
+//    16.4 us against 19.0 with the next one, that of 16384 51-56 against 38 when
+//    both were first built);
 //  - up to kMergeIds two: tiles of kMergeTile ids are sorted by that count,
 //    then an id's place is the sum of its places in all tiles, each found by a
-//    binary search in LDS (8011 ids: 5 + 6 us, against 22 us for the radix
+//    binary search in LDS (8011 ids: 5 + 5 us, against 22 us for the radix
 //    sort's four launches);
 //  - beyond that a radix sort, least significant digit first, of a count and a
 //    scatter per pass; a workgroup of NT threads takes a tile of NT *
@@ -241,8 +242,8 @@ __global__ __launch_bounds__(256) void lookup_kernel(const TI* __restrict__ tabl
 //    over many CUs, 4096 beyond (1 M ids: 5 + 5 + 13 us a pass).
 //
 // The sort leaves HBM idle, so the launches that place pairs carry workgroups
-// behind their own that write the table's zeros (16384 ids, 77 MB of zeros: 19 us
-// for both against 10 + 11 us one after the other).
+// behind their own that write the table's zeros (16384 ids, 77 MB of zeros: 16 us
+// for both, of which the zeros alone take 11).
 
 constexpr int kRankIds = 4096;
 constexpr int kRankWaves = 16;
@@ -467,6 +468,22 @@ __device__ __forceinline__ uint32_t count_below(u32x4 k, uint32_t below) {
   return static_cast<uint32_t>(__popc(signs));
 }
 
+// keys[0 .. padded) = key(j), kNoKey behind the n-th, by a workgroup of kRankWaves
+// waves.  U loads of a thread are on their way at once (behind the last key it is
+// read again): one after the other they cost the merge of 16384 ids 3 us of 12.
+template <int U, typename F>
+__device__ __forceinline__ void load_keys(uint32_t* keys, int padded, int n, F key) {
+  constexpr int step = kRankWaves * 64;
+  for (int j0 = threadIdx.x; j0 < padded; j0 += U * step) {
+    uint32_t k[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) k[u] = key(j0 + u * step < n ? j0 + u * step : n - 1);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (j0 + u * step < padded) keys[j0 + u * step] = j0 + u * step < n ? k[u] : kNoKey;
+  }
+}
+
 // The places of kRankLanes ids per workgroup among all n <= kRankIds.  The keys
 // lie in LDS; each wave compares its share of them with the ids, its lanes in
 // groups that take every G-th run of four keys.
@@ -485,8 +502,8 @@ __global__ __launch_bounds__(kRankWaves * 64) void rank_kernel(SortSrc src, int 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int padded = (n + kPart - 1) / kPart * kPart;
-  for (int j = threadIdx.x; j < padded; j += kRankWaves * 64)
-    keys[j] = j < n ? sort_pair(src, j)[0] : kNoKey;
+  load_keys<kRankIds / (kRankWaves * 64)>(keys, padded, n,
+                                          [&](int j) { return sort_pair(src, j)[0]; });
   __syncthreads();
   const int first = blockIdx.x * I;          // a multiple of G * 4
   const int i = first + lane % I, group = lane / I;
@@ -560,9 +577,7 @@ __global__ __launch_bounds__(kRankWaves * 64) void merge_tiles_kernel(
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles = (n + kMergeTile - 1) / kMergeTile;
-#pragma unroll 4
-  for (int j = threadIdx.x; j < tiles * kMergeTile; j += kRankWaves * 64)
-    keys[j] = j < n ? pairs[j][0] : kNoKey;
+  load_keys<8>(keys, tiles * kMergeTile, n, [&](int j) { return pairs[j][0]; });
   const int i = blockIdx.x * 64 + lane, own = blockIdx.x * 64 / kMergeTile;
   u32x2 pair = {0, 0};
   if (i < n) pair = pairs[i];
