@@ -1633,33 +1633,43 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs
     return;
   }
   // By the last wave, which has the fewest vectors, beside the exponentials:
-  // each listed token's whole p, in its first entry, and who stores it.
+  // who stores each entry's token, and the token's whole p.  Entries of one token
+  // have one owner, so only those that share theirs are compared.  Each of them
+  // gets the whole p and is stored, the same value each time.
   if (GRAD && threadIdx.x >= NT - 64) {
+    int owner[M];
     float all[M];
-    bool first[M];
 #pragma unroll
     for (int j = 0; j < M; ++j) {
       const int q = j * 64 + lane;
-      first[j] = q < a.k && id[q] >= 0;
-      all[j] = 0.0f;
-      if (first[j]) {
-        for (int f = 0; f < a.k; ++f) {
-          if (id[f] == id[q]) {
-            all[j] += p[f];
-            first[j] = first[j] && f >= q;
-          }
-        }
+      owner[j] = q < a.k && id[q] >= 0 ? r.owner(id[q]) : -1;
+      all[j] = owner[j] >= 0 ? p[q] : 0.0f;
+      if (owner[j] >= 0) next[q] = atomicExch(&mail[owner[j]], q);
+    }
+    wave_fence();
+    uint64_t shared[M];
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int q = j * 64 + lane;
+      const bool with = owner[j] >= 0 && (mail[owner[j]] != q || next[q] != kNone);
+      if (with) all[j] = 0.0f;
+      shared[j] = __ballot(with);
+    }
+#pragma unroll
+    for (int g = 0; g < M; ++g) {
+      for (uint64_t left = shared[g]; left != 0; left &= left - 1) {
+        const int f = g * 64 + __builtin_ctzll(left);
+        const int32_t token = id[f];
+        const float pf = p[f];
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+          if ((shared[j] >> lane & 1) != 0 && id[j * 64 + lane] == token) all[j] += pf;
       }
     }
     wave_fence();
 #pragma unroll
-    for (int j = 0; j < M; ++j) {
-      const int q = j * 64 + lane;
-      if (first[j]) {
-        p[q] = all[j];
-        next[q] = atomicExch(&mail[r.owner(id[q])], q);
-      }
-    }
+    for (int j = 0; j < M; ++j)
+      if (owner[j] >= 0) p[j * 64 + lane] = all[j];
   }
   const Exponent e(m, a.inv_tau);
   float sum[1] = {0.0f};
