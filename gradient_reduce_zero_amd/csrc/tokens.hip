@@ -1037,7 +1037,8 @@ template <typename T, int NT, int NV, bool ONCE = false> struct Row {
       for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]);
     }
   }
-  // f(vector's elements, index of the first) for each of this thread's vectors.
+  // f(vector's elements, index of the first, which of the thread's it is) for each
+  // of this thread's vectors.
   template <typename F> __device__ __forceinline__ void vectors(F f) const {
     float x[E];
     if constexpr (NV > 0) {
@@ -1046,30 +1047,33 @@ template <typename T, int NT, int NV, bool ONCE = false> struct Row {
         const int v = j * NT + static_cast<int>(threadIdx.x);
         if (v < nvec) {
           unpack(kept[j], x);
-          f(x, head + v * E);
+          f(x, head + v * E, j);
         }
       }
     } else {
-      for (int v = threadIdx.x; v < nvec; v += NT) {
+      for (int v = threadIdx.x, j = 0; v < nvec; v += NT, ++j) {
         unpack(*reinterpret_cast<const u32x4*>(p + head + v * E), x);
-        f(x, head + v * E);
+        f(x, head + v * E, j);
       }
     }
   }
   // f(x, index) for each of this thread's elements.
   template <typename F> __device__ __forceinline__ void each(F f) const {
-    vectors([&](float (&x)[E], int at) {
+    vectors([&](float (&x)[E], int at, int) {
 #pragma unroll
       for (int i = 0; i < E; ++i) f(x[i], at + i);
     });
     if (edge >= 0) f(edge_x, edge);
   }
-  // dst[index] = f(x) over the row; dst may be the row itself.
-  template <typename F> __device__ __forceinline__ void map(T* dst, F f) const {
+  // dst[index] = f(x) over the row; dst may be the row itself.  last(values, index
+  // of the first, which of the thread's vectors) may change a vector's.
+  template <typename F, typename L>
+  __device__ __forceinline__ void map(T* dst, F f, L last) const {
     const bool vec = reinterpret_cast<uintptr_t>(dst + head) % 16 == 0;
-    vectors([&](float (&x)[E], int at) {
+    vectors([&](float (&x)[E], int at, int j) {
 #pragma unroll
       for (int i = 0; i < E; ++i) x[i] = f(x[i]);
+      last(x, at, j);
       if (vec) {
         store_vec<T, E, true>(dst + at, x);
       } else {
@@ -1215,10 +1219,10 @@ __device__ __forceinline__ void each_exponent(const R& r, const Exponent& e, F f
   if (e.plain) r.each([&](float x, int) { f(e.near(x)); });
   else r.each([&](float x, int) { f(e.far(x)); });
 }
-template <typename R, typename T, typename F>
-__device__ __forceinline__ void map_exponent(const R& r, T* dst, const Exponent& e, F f) {
-  if (e.plain) r.map(dst, [&](float x) { return f(e.near(x)); });
-  else r.map(dst, [&](float x) { return f(e.far(x)); });
+template <typename R, typename T, typename F, typename L>
+__device__ __forceinline__ void map_exponent(const R& r, T* dst, const Exponent& e, F f, L last) {
+  if (e.plain) r.map(dst, [&](float x) { return f(e.near(x)); }, last);
+  else r.map(dst, [&](float x) { return f(e.far(x)); }, last);
 }
 
 // The order of the top list: larger values first, then lower indices, as one
@@ -1386,7 +1390,7 @@ __device__ __forceinline__ void top_list(const Row<T, NT, NV, ONCE>& r, int voca
         wave_fence();
       }
     } else {
-      r.vectors([&](float (&x)[E], int at) { add_candidates(x, at, bound, lds); });
+      r.vectors([&](float (&x)[E], int at, int) { add_candidates(x, at, bound, lds); });
     }
     if (!every && r.edge >= 0) {
       const float x[1] = {r.edge_x};
@@ -1503,7 +1507,7 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void logprob_kernel(LogprobArgs
       const float lq = d - log2s;
       return -__builtin_amdgcn_exp2f(lq) * fmaf(slope, fmaxf(lq, kLowest), base);
     };
-    map_exponent(r, dx, e, value);
+    map_exponent(r, dx, e, value, [](auto&, int, int) {});
     // Over what its thread has just stored.
     if (given && r.owner(static_cast<int>(target)) == static_cast<int>(threadIdx.x))
       put(dx + target, glp + value(e.of(xt)));
@@ -1542,13 +1546,14 @@ template <typename T> struct DistillArgs {
 //
 // The first wave holds the list, two entries per lane; its loads go out before
 // the row's, so that the list is ready when the row comes.  A listed element's
-// gradient is stored by the thread that holds it, over what it has stored
-// before: a thread finds its entries through `mail`, and no wave has to wait for
-// another's stores (4096 x 50257 bf16, 32 listed: 151 us, 5.5 TB/s, against 167 us
-// with the list read behind the row and its elements stored behind a barrier).
+// gradient is put into its vector by the thread that holds it, which finds its
+// entries through `mail`: stored by itself, behind the vector, each costs HBM a
+// partial write (8192 x 32000 bf16, 64 listed: 193 us, 5.4 TB/s, against 211 us;
+// 4096 x 50257, 32 listed: 145 against 149).  One listed token takes 191 us there,
+// 128 take 206.
 template <typename T, int NT, int NV, bool GRAD>
 __global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs<T> a) {
-  constexpr int M = GRZ_MAX_TOP / 64, kNone = 255;
+  constexpr int M = GRZ_MAX_TOP / 64, kNone = 255, E = Row<T, NT, NV>::E;
   __shared__ float lds_max[NT / 64];
   __shared__ float lds_sum[NT / 64][1];
   __shared__ int32_t id[GRZ_MAX_TOP];
@@ -1693,9 +1698,22 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs
   if constexpr (GRAD) {
     const float c = w * a.grad_scale * a.tau;
     auto q_of = [&](float d) { return __builtin_amdgcn_exp2f(d - log2s); };
-    map_exponent(r, dx, e, [&](float d) { return c * q_of(d); });
-    for (int q = mail[threadIdx.x]; q != kNone; q = next[q])
-      put(dx + id[q], c * (q_of(e.of(xl[q])) - p[q]));
+    auto listed_of = [&](int q) { return c * (q_of(e.of(xl[q])) - p[q]); };
+    const int mine = mail[threadIdx.x];
+    uint32_t hit = 0;  // which of the thread's vectors hold listed tokens, modulo 32
+    for (int q = mine; q != kNone; q = next[q]) hit |= 1u << ((id[q] - r.head) / (E * NT) & 31);
+    map_exponent(r, dx, e, [&](float d) { return c * q_of(d); },
+                 [&](float (&x)[E], int at, int j) {
+      if ((hit >> (j & 31) & 1) == 0) return;
+      for (int q = mine; q != kNone; q = next[q]) {
+        const int in = id[q] - at;
+        const float value = listed_of(q);
+#pragma unroll
+        for (int i = 0; i < E; ++i) x[i] = in == i ? value : x[i];
+      }
+    });
+    for (int q = mine; q != kNone; q = next[q])
+      if (id[q] == r.edge) put(dx + id[q], listed_of(q));
   }
 }
 
