@@ -990,7 +990,8 @@ __global__ __launch_bounds__(kDirectWaves * 64) void direct_grad_kernel(
 //
 // NV > 0: the row is read once and kept in registers, up to NV vectors per
 // thread, so that its maximum, its sums and its gradient cost one pass over
-// HBM.  NV = 0, for rows too long for that: each step reads the row again.
+// HBM.  NV = 0, for rows too long for that: one pass for the maximum and the sums
+// and one for the gradient or the top list.
 //
 // ONCE: nothing reads the row again after this load (non-temporal).
 
@@ -1104,6 +1105,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // 2^d underflows to zero far above this, so terms of 2^d * d can be cut here:
 // 0 * -inf (a masked element) becomes 0.
 constexpr float kLowest = -1.0e4f;
+constexpr float kLowestFloat = -3.402823466e38f;
 
 // Reductions.  A wave's in a fixed tree: four steps of lane exchanges inside
 // each row of 16 lanes, then the four rows.
@@ -1190,9 +1192,8 @@ __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* lds) {
 }
 
 // Waves per SIMD the kernels are built for: two workgroups of 1024 threads on a
-// CU, so that one's loads and stores run beside the other's arithmetic; with
-// 16 vectors kept the registers hold one.
-constexpr int kept_waves(int nv) { return nv > 8 ? 4 : 8; }
+// CU, so that one's loads and stores run beside the other's arithmetic.
+constexpr int kRowWaves = 8;
 
 // The row's exponents, in powers of two: an element's is x * l2 - at, l2 =
 // log2(e) / T, with one fused rounding.  `at` = max * l2, rounded (by at most
@@ -1202,8 +1203,8 @@ constexpr int kept_waves(int nv) { return nv > 8 ? 4 : 8; }
 struct Exponent {
   float inv_tau, l2, max, at;
   bool plain;
-  __device__ __forceinline__ Exponent(float m, float inv)
-      : inv_tau(inv), l2(kLog2e * inv), max(m), at(m * l2), plain(fabsf(at) < 1.0e6f) {}
+  __device__ __forceinline__ Exponent(float m, float inv, bool fused)
+      : inv_tau(inv), l2(kLog2e * inv), max(m), at(m * l2), plain(fused && fabsf(at) < 1.0e6f) {}
   __device__ __forceinline__ float far(float x) const { return (x - max) * l2; }
   __device__ __forceinline__ float near(float x) const { return fmaf(x, l2, -at); }
   __device__ __forceinline__ float of(float x) const { return plain ? near(x) : far(x); }
@@ -1223,6 +1224,44 @@ template <typename R, typename T, typename F, typename L>
 __device__ __forceinline__ void map_exponent(const R& r, T* dst, const Exponent& e, F f, L last) {
   if (e.plain) r.map(dst, [&](float x) { return f(e.near(x)); }, last);
   else r.map(dst, [&](float x) { return f(e.far(x)); }, last);
+}
+
+// The largest of a thread's elements, with S = sum 2^d and (where A) A = sum 2^d d,
+// d counted from it, in one pass: a larger element that comes later shifts what
+// has been summed.  For rows that are not kept in registers.
+__device__ __forceinline__ void shift_sums(float by, float& s, float& a) {
+  by = fmaxf(by, kLowest);  // from a thread whose elements are all masked: s = a = 0
+  const float f = __builtin_amdgcn_exp2f(by);
+  a = f * fmaf(by, s, a);
+  s *= f;
+}
+template <bool A, typename R>
+__device__ __forceinline__ float running_sums(const R& r, float l2, float& s, float& a) {
+  float max = -INFINITY, from = kLowestFloat;  // `from` stays finite while all are masked
+  auto add = [&](auto& x) {
+    float most = x[0];
+    for (float v : x) most = fmaxf(most, v);
+    max = fmaxf(max, most);
+    if (most > from) {
+      shift_sums((from - most) * l2, s, a);
+      from = most;
+    }
+    for (float v : x) {
+      const float d = (v - from) * l2, p = __builtin_amdgcn_exp2f(d);
+      s += p;
+      if (A) a = fmaf(p, fmaxf(d, kLowest), a);
+    }
+  };
+  r.vectors([&](auto& x, int, int) { add(x); });
+  if (r.edge >= 0) {
+    const float x[1] = {r.edge_x};
+    add(x);
+  }
+  return max;
+}
+// Such a thread's sums, counted from the row's largest element.
+__device__ __forceinline__ void join_sums(const Exponent& e, float own_max, float& s, float& a) {
+  shift_sums((fmaxf(own_max, kLowestFloat) - e.max) * e.l2, s, a);
 }
 
 // The order of the top list: larger values first, then lower indices, as one
@@ -1389,7 +1428,7 @@ __device__ __forceinline__ void top_list(const Row<T, NT, NV, ONCE>& r, int voca
         }
         wave_fence();
       }
-    } else {
+    } else if (own_max >= bound) {
       r.vectors([&](float (&x)[E], int at, int) { add_candidates(x, at, bound, lds); });
     }
     if (!every && r.edge >= 0) {
@@ -1453,10 +1492,10 @@ template <typename T> struct LogprobArgs {
 // 30-50 % with half of the row masked.
 //
 // Bound by HBM: 4096 x 50257 bf16 in 68 us (6.1 TB/s), its gradient in 153 us, that
-// of 8192 x 32000 in 183 us (5.7 TB/s, reads and writes mixed); one workgroup of 256
+// of 8192 x 32000 in 187 us (5.6 TB/s, reads and writes mixed); one workgroup of 256
 // threads reading the row for each step took 307-315 us for such gradients.
 template <typename T, int NT, int NV, bool GRAD>
-__global__ __launch_bounds__(NT, kept_waves(NV)) void logprob_kernel(LogprobArgs<T> a) {
+__global__ __launch_bounds__(NT, kRowWaves) void logprob_kernel(LogprobArgs<T> a) {
   __shared__ float lds_max[NT / 64];
   __shared__ float lds_sum[NT / 64][2];
   const int64_t i = a.row0 + blockIdx.x;
@@ -1476,17 +1515,21 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void logprob_kernel(LogprobArgs
   const T* row = a.x + i * a.stride;
   const Row<T, NT, NV, true> r(row, a.vocab);
   const float xt = given ? widen(row[target]) : 0.0f;
-  float own_max = -INFINITY;
-  r.each([&](float x, int) { own_max = fmaxf(own_max, x); });
+  const bool spread = a.entropy != nullptr || (GRAD && gent != 0.0f);  // A is needed
+  float own_max = -INFINITY, sum[2] = {0.0f, 0.0f};
+  if constexpr (NV > 0) r.each([&](float x, int) { own_max = fmaxf(own_max, x); });
+  else if (spread) own_max = running_sums<true>(r, kLog2e, sum[0], sum[1]);
+  else own_max = running_sums<false>(r, kLog2e, sum[0], sum[1]);
   extern __shared__ u32x4 top_memory[];  // with a top list
   TopLds<NT, NV>& lds_top = *reinterpret_cast<TopLds<NT, NV>*>(top_memory);
   if (!GRAD && a.top > 0) top_groups(own_max, lds_top);
-  const Exponent e(block_max<NT>(own_max, lds_max), 1.0f);
+  const Exponent e(block_max<NT>(own_max, lds_max), 1.0f, NV > 0);
   if (NT == 64) __syncthreads();
   if (!GRAD && a.top > 0 && threadIdx.x >= NT - 64 && (NT > 64 || a.vocab > kAllListed))
     top_bound(a.top, lds_top);
-  float sum[2] = {0.0f, 0.0f};
-  if (a.entropy != nullptr || (GRAD && gent != 0.0f)) {
+  if constexpr (NV == 0) {
+    join_sums(e, own_max, sum[0], sum[1]);
+  } else if (spread) {
     each_exponent(r, e, [&](float d) {
       const float p = __builtin_amdgcn_exp2f(d);
       sum[0] += p;
@@ -1559,7 +1602,7 @@ template <typename T> struct DistillArgs {
 // 4096 x 50257, 32 listed: 145 against 149).  One listed token takes 191 us there,
 // 128 take 206.
 template <typename T, int NT, int NV, bool GRAD>
-__global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs<T> a) {
+__global__ __launch_bounds__(NT, kRowWaves) void distill_kernel(DistillArgs<T> a) {
   constexpr int M = GRZ_MAX_TOP / 64, kNone = 255, E = Row<T, NT, NV>::E;
   __shared__ float lds_max[NT / 64];
   __shared__ float lds_sum[NT / 64][1];
@@ -1635,10 +1678,11 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs
     }
     if (lane == 0) listed = some;
   }
-  float m = -INFINITY;
-  r.each([&](float x, int) { m = fmaxf(m, x); });
+  float own_max = -INFINITY, sum[1] = {0.0f}, unused = 0.0f;
+  if constexpr (NV > 0) r.each([&](float x, int) { own_max = fmaxf(own_max, x); });
+  else own_max = running_sums<false>(r, kLog2e * a.inv_tau, sum[0], unused);
   if constexpr (NT == 64) __syncthreads();
-  m = block_max<NT>(m, lds_max);  // its barrier also publishes the list
+  const float m = block_max<NT>(own_max, lds_max);  // its barrier also publishes the list
   if (!listed) {
     if (threadIdx.x == 0 && a.loss != nullptr) a.loss[i] = 0.0f;
     if constexpr (GRAD) zero_row<T, NT>(dx, a.vocab);
@@ -1683,9 +1727,9 @@ __global__ __launch_bounds__(NT, kept_waves(NV)) void distill_kernel(DistillArgs
     for (int j = 0; j < M; ++j)
       if (owner[j] >= 0) p[j * 64 + lane] = all[j];
   }
-  const Exponent e(m, a.inv_tau);
-  float sum[1] = {0.0f};
-  each_exponent(r, e, [&](float d) { sum[0] += __builtin_amdgcn_exp2f(d); });
+  const Exponent e(m, a.inv_tau, NV > 0);
+  if constexpr (NV == 0) join_sums(e, own_max, sum[0], unused);
+  else each_exponent(r, e, [&](float d) { sum[0] += __builtin_amdgcn_exp2f(d); });
   if (GRAD && threadIdx.x < 64) {
 #pragma unroll
     for (int j = 0; j < M; ++j)
@@ -1742,14 +1786,16 @@ int row_launch(void (*kernel)(Args), int threads, size_t lds, Args a, int64_t n,
 // that two workgroups of 1024 (or four of 512, ...) share a CU.  The gradient of
 // 4096 x 50257 logits: 154 us with 1024 threads of 8 vectors, 162 with 512 of 13
 // (three workgroups on a CU), 174 with 256 of 25 (four).  One wave per row up to
-// 256 vectors (its lists are at most 64 long).
+// 256 vectors (its lists are at most 64 long).  Rows of more vectors are read
+// again: kept by 1024 threads of 16, which leaves one workgroup on a CU, 1024 x
+// 128000 took 68 us instead of 50, their distillation loss 59 instead of 48, their
+// gradient 115 instead of 125.
 #define GRZ_ROW_SHAPES(CALL)                                  \
   const int64_t vectors = a.vocab / (16 / (int)sizeof(T));    \
   if (vectors <= 64 * 4 && a.top <= 64) return CALL(64, 4);   \
   if (vectors <= 256 * 8) return CALL(256, 8);                \
   if (vectors <= 512 * 8) return CALL(512, 8);                \
   if (vectors <= 1024 * 8) return CALL(1024, 8);              \
-  if (vectors <= 1024 * 16) return CALL(1024, 16);            \
   return CALL(1024, 0);
 
 template <typename T, bool GRAD>

@@ -339,6 +339,46 @@ def test_logprobs_of_rows_without_a_softmax(v, dtype):
     assert ids[0].tolist() == list(range(6)) and ids[1, 0] == 7 and ids[2, :2].tolist() == [9, 11]
 
 
+@pytest.mark.parametrize("v,dtype", [(66003, BF16), (33003, F32), (140001, BF16), (70001, F32)])
+def test_logprobs_of_long_rows_in_any_order(v, dtype):
+    # Rows too long for the registers: their sums follow a maximum that moves.
+    x = logits_of(12, v, dtype)
+    x[0] = torch.linspace(-60, 60, v, device=DEV).to(dtype)      # it moves all the time
+    x[1] = x[0].flip(0)
+    x[2, : v - 9] = -math.inf                                    # most threads see masks only
+    x[3, : v // 2] = -math.inf                                   # masks first
+    x[4, ::2] = LOWEST[dtype]
+    x[5].fill_(LOWEST[dtype])
+    x[6] = 1e30 * x[6]
+    x[7, : v // 2] = -3e38                                       # differences overflow
+    x[7, v // 2:] = 3e38
+    x[8] = 2.5
+    x[9].fill_(-math.inf)
+    x[10, v - 2] = math.nan
+    x[11, v - 1] = math.inf
+    targets = torch.arange(12, device=DEV)
+    targets[2] = targets[3] = v - 4
+    check_logprobs(x[:9], targets[:9], 25, "rows")
+    lp, h, ids, tl = logprob_call(x, targets, 25)
+    assert torch.isnan(lp[9:]).all() and torch.isnan(h[9:]).all() and torch.isnan(tl[9:]).all()
+    assert torch.equal(ids.cpu().long(), order_of(x, 25))
+    glp = torch.linspace(-1, 1, 9, device=DEV)
+    gent = torch.linspace(0.5, -0.5, 9, device=DEV)
+    dx = torch.empty_like(x[:9])
+    grz.dp_token_logprobs_grad(x[:9], targets[:9], glp, gent, dx)
+    want, tol = ref.logprob_grad(x[:9], targets[:9], glp, gent)
+    ref.assert_close(dx, want, tol, "dlogits")
+    k = torch.arange(0, v, v // 30, device=DEV)[:30].expand(9, 30).contiguous()
+    keep = [0, 1, 4, 5, 6, 8]                # a listed masked token has no finite loss
+    y, k = x[keep].contiguous(), k[keep].contiguous()
+    z = torch.randn(len(keep), 30, device=DEV, generator=gen(26))
+    loss, dy = torch.empty(len(keep), device=DEV), torch.empty_like(y)
+    grz.dp_distill_grad(y, k, z, dy, temperature=2.0, loss=loss)
+    d = ref.Distill(y, k, z, 2.0)
+    ref.assert_close(loss, d.loss, d.loss_tol, "loss")
+    ref.assert_close(dy, d.dx, d.dx_tol, "distillation's dlogits")
+
+
 def test_logprobs_outputs_may_be_left_out():
     x = logits_of(5, 777, BF16)
     t = token_ids(5, 777, 22)

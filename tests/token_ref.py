@@ -160,7 +160,10 @@ def embed_grad(dout, ids, vocab, scale, old=None):
 
 def assert_close(got, want, tol, what, dtype=None):
     """|got - want| <= tol plus the rounding to ``dtype`` of a value up to tol off;
-    non-finite values agree in kind."""
+    non-finite values agree in kind.  A wanted value beyond the largest fp32 number,
+    (2 - 2^-23) 2^127, by more than half a step, i.e. from (2 - 2^-24) 2^127 on, is an
+    infinity in fp32: -3e38 less 3e38 cannot be anything else."""
+    want = torch.where(want.abs() >= (2 - U) * 2.0 ** 127, torch.sign(want) * math.inf, want)
     got = got.detach().cpu()
     dtype = dtype or got.dtype
     got = got.double()
