@@ -1454,15 +1454,16 @@ __device__ __forceinline__ void top_list(const Row<T, NT, NV, ONCE>& r, int voca
     }
   }
   const Row<T, NT, 0> again(r.p, vocab);
-  uint64_t last = ~0ull;
+  uint64_t most = ~0ull;  // the next place's order at most; a NaN at token 0 has this one
   for (int k = 0; k < top; ++k) {
     uint64_t best = 0;
     again.each([&](float x, int index) {
       const uint64_t o = order_of(x, index);
-      if (o < last && o > best) best = o;
+      if (o <= most && o > best) best = o;
     });
-    last = block_max<NT>(best, lds.best);
-    if (threadIdx.x == 0) emit(k, last);
+    best = block_max<NT>(best, lds.best);
+    if (threadIdx.x == 0) emit(k, best);
+    most = best - 1;  // best > 0: no order is 0, and top <= vocab
   }
 }
 
