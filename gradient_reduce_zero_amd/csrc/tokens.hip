@@ -1826,6 +1826,48 @@ int check_pair(const void* x, int dtype, int64_t n, int64_t vocab, int64_t strid
              ? GRZ_EINVAL : GRZ_OK;
 }
 
+// A flat array of a call over the vocabulary; absent: no bytes.
+struct Flat {
+  const void* at;
+  size_t bytes;
+  bool row_value;  // one fp32 value a row
+  Flat(const void* p, int64_t count, size_t size, bool row = false)
+      : at(p), bytes(p != nullptr ? static_cast<size_t>(count) * size : 0), row_value(row) {}
+};
+Flat row_values(const float* p, int64_t n) { return Flat(p, n, 4, true); }
+
+// Whether an array lies over elements of a row matrix; what lies between the rows
+// is the caller's.
+bool covers(const void* x, int dtype, int64_t rows, int64_t cols, int64_t stride, const Flat& f) {
+  if (!overlap(x, span_of(dtype, rows, cols, stride), f.at, f.bytes)) return false;
+  const uintptr_t base = reinterpret_cast<uintptr_t>(x), at = reinterpret_cast<uintptr_t>(f.at);
+  if (at <= base) return true;
+  const size_t step = elem_size(dtype) * static_cast<size_t>(stride), in = (at - base) % step;
+  return in < elem_size(dtype) * static_cast<size_t>(cols) || in + f.bytes > step;
+}
+
+// The outputs may not lie over an input or each other: workgroups write their rows
+// while others still read theirs.  dlogits over the logits: check_pair.  A value a
+// row may replace one that comes in: its row's workgroup has read that by then.
+template <size_t I, size_t O>
+int check_outputs(const void* logits, const void* dlogits, int dtype, int64_t n, int64_t vocab,
+                  int64_t stride, int64_t dstride, const Flat (&in)[I], const Flat (&out)[O]) {
+  for (const Flat& f : in)
+    if (covers(dlogits, dtype, dlogits != nullptr ? n : 0, vocab, dstride, f)) return GRZ_EINVAL;
+  for (size_t o = 0; o < O; ++o) {
+    const Flat& f = out[o];
+    if (covers(logits, dtype, n, vocab, stride, f) ||
+        covers(dlogits, dtype, dlogits != nullptr ? n : 0, vocab, dstride, f))
+      return GRZ_EINVAL;
+    for (const Flat& i : in)
+      if (overlap(i.at, i.bytes, f.at, f.bytes) && !(i.at == f.at && i.row_value && f.row_value))
+        return GRZ_EINVAL;
+    for (size_t k = 0; k < o; ++k)
+      if (overlap(out[k].at, out[k].bytes, f.at, f.bytes)) return GRZ_EINVAL;
+  }
+  return GRZ_OK;
+}
+
 template <typename T>
 int logprobs_entry(const void* logits, int64_t n, int64_t vocab, int64_t stride,
                    const void* targets, int id_bits, int top, float* logprob, float* entropy,
@@ -1872,6 +1914,11 @@ int distill_entry(const void* logits, int dtype, int64_t n, int64_t vocab, int64
   } else if (loss == nullptr) {
     return GRZ_EINVAL;
   }
+  const Flat in[] = {Flat(ids, n * k, id_bits / 8), Flat(teacher, n * k, elem_size(teacher_dtype)),
+                     row_values(weights, n)};
+  const Flat out[] = {row_values(loss, n)};
+  if ((st = check_outputs(logits, dlogits, dtype, n, vocab, stride, dstride, in, out)) != GRZ_OK)
+    return st;
   return dtype == GRZ_BF16
              ? distill_run<uint16_t>(logits, n, vocab, stride, ids, id_bits, teacher,
                                      teacher_dtype, k, temperature, weights, grad_scale, loss,
@@ -2216,6 +2263,11 @@ int dp_token_logprobs(const void* logits, int dtype, int64_t n, int64_t vocab, i
   if (check_list(logprob) != GRZ_OK || check_list(entropy) != GRZ_OK ||
       check_list(top_logprobs) != GRZ_OK || (top_ids != nullptr && !aligned(top_ids, 4)))
     return GRZ_EALIGN;
+  const Flat in[] = {Flat(targets, n, id_bits / 8)};
+  const Flat out[] = {row_values(logprob, n), row_values(entropy, n), Flat(top_ids, n * top, 4),
+                      Flat(top_logprobs, n * top, 4)};
+  if ((st = check_outputs(logits, nullptr, dtype, n, vocab, stride, 0, in, out)) != GRZ_OK)
+    return st;
   return dtype == GRZ_BF16
              ? logprobs_entry<uint16_t>(logits, n, vocab, stride, targets, id_bits, top, logprob,
                                         entropy, top_ids, top_logprobs, nullptr, nullptr, nullptr,
@@ -2240,6 +2292,12 @@ int dp_token_logprobs_grad(const void* logits, int dtype, int64_t n, int64_t voc
       check_list(glogprob) != GRZ_OK || check_list(gentropy) != GRZ_OK)
     return GRZ_EALIGN;
   if ((st = check_pair(logits, dtype, n, vocab, stride, dlogits, dlogits_stride)) != GRZ_OK)
+    return st;
+  const Flat in[] = {Flat(targets, n, id_bits / 8), row_values(glogprob, n),
+                     row_values(gentropy, n)};
+  const Flat out[] = {row_values(logprob, n), row_values(entropy, n)};
+  if ((st = check_outputs(logits, dlogits, dtype, n, vocab, stride, dlogits_stride, in, out)) !=
+      GRZ_OK)
     return st;
   return dtype == GRZ_BF16
              ? logprobs_entry<uint16_t>(logits, n, vocab, stride, targets, id_bits, 0, logprob,

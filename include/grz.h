@@ -577,8 +577,11 @@ int zero1_fused_step_args(const void* const* rank_grads, int nranks, int dtype,
  *    values gives the same bits; the order of a vocabulary row's sums follows
  *    its place on the 16-byte borders, so another layout may round otherwise.
  *  - Errors, beside each entry point's own: GRZ_EINVAL for a null pointer, a
- *    type or flag that is not taken, or an output matrix (or workspace) that
- *    overlaps an input matrix; GRZ_EALIGN; GRZ_ERANGE.
+ *    type or flag that is not taken, or an output (or workspace) that overlaps
+ *    an input or another output (two matrices do if their spans, first to last
+ *    element, do); GRZ_EALIGN; GRZ_ERANGE.  Two overlaps are taken: dlogits
+ *    that are the logits, and a logprob, entropy or loss array that is the same
+ *    array as glogprob, gentropy or weights.
  */
 
 /*

@@ -31,3 +31,66 @@ def test_top_list_of_rows_with_a_nan_at_the_first_token(v, dtype):
         lp, h, ids, tl = logprob_call(x, t, top)
         assert torch.equal(ids.cpu().long(), order_of(x, top)), top
         assert torch.isnan(lp).all() and torch.isnan(h).all() and torch.isnan(tl).all()
+
+
+@pytest.mark.parametrize("v", [65, 3000, 33000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_values_written_over_the_ones_that_come_in(v, dtype):
+    # One value a row: its row has read what came in before it writes.
+    n, k = 2000 if v < 33000 else 600, 5
+    g = torch.Generator(device=DEV).manual_seed(80)
+    x = logits_of(n, v, dtype)
+    t = torch.randint(-1, v, (n,), device=DEV, generator=g)
+    a, b = (torch.randn(n, device=DEV, generator=g) for _ in range(2))
+    a[::7] = 0.0
+    b[::7] = 0.0
+    dx, lp, h = torch.empty_like(x), torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    grz.dp_token_logprobs_grad(x, t, a, b, dx, logprob=lp, entropy=h)
+    for first in (False, True):  # each value over either one
+        a2, b2, dx2 = a.clone(), b.clone(), torch.empty_like(x)
+        lp2, h2 = (a2, b2) if first else (b2, a2)
+        grz.dp_token_logprobs_grad(x, t, a2, b2, dx2, logprob=lp2, entropy=h2)
+        assert torch.equal(dx2, dx) and torch.equal(lp2, lp) and torch.equal(h2, h)
+    ids = torch.randint(-1, v, (n, k), device=DEV, generator=g)
+    z = torch.randn(n, k, device=DEV, generator=g)
+    loss, only = torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    grz.dp_distill_grad(x, ids, z, dx, temperature=2.0, weights=a, loss=loss)
+    grz.dp_distill_loss(x, ids, z, only, temperature=2.0, weights=a)
+    w, dx2 = a.clone(), torch.empty_like(x)
+    grz.dp_distill_grad(x, ids, z, dx2, temperature=2.0, weights=w, loss=w)
+    assert torch.equal(dx2, dx) and torch.equal(w, loss)
+    w = a.clone()
+    grz.dp_distill_loss(x, ids, z, w, temperature=2.0, weights=w)
+    assert torch.equal(w, only)
+
+
+def test_arrays_between_the_rows_of_the_logits():
+    # What lies between a matrix's rows is the caller's, its lists among it.
+    n, v, stride, k = 3, 1000, 1064, 4
+    buf = torch.zeros(n * stride, device=DEV)
+    x = torch.as_strided(buf, (n, v), (stride, 1))
+    x.copy_(logits_of(n, v, F32))
+
+    def gap(row, at, *shape):
+        return torch.as_strided(buf, shape, (shape[1], 1) if len(shape) == 2 else (1,),
+                                row * stride + v + at)
+
+    loss, w, z = gap(0, 0, n), gap(0, 60, n), gap(1, 50, n, k)
+    lp, h, tl = gap(1, 0, n), gap(1, 4, n), gap(1, 10, n, k)
+    w.fill_(1.5)
+    z.normal_()
+    ids = torch.arange(n * k, device=DEV).view(n, k)
+    t = torch.arange(n, device=DEV)
+    want = [torch.empty(n, device=DEV) for _ in range(3)]
+    top, top2 = (torch.empty(n, k, device=DEV, dtype=torch.int32) for _ in range(2))
+    wtl, dx = torch.empty(n, k, device=DEV), torch.empty(n, v, device=DEV)
+    y = x.clone()
+    grz.dp_token_logprobs(y, t, want[0], want[1], top, wtl)
+    grz.dp_distill_grad(y, ids, z.clone(), dx, weights=w.clone(), loss=want[2])
+    grz.dp_token_logprobs(x, t, lp, h, top2, tl)
+    assert torch.equal(top, top2)
+    grz.dp_distill_grad(x, ids, z, x, weights=w, loss=loss)
+    for got, one in ((lp, want[0]), (h, want[1]), (tl, wtl), (loss, want[2]), (x, dx)):
+        assert torch.equal(got, one)
+    with pytest.raises(grz.GrzError):  # one place further it reaches the next row
+        grz.dp_distill_grad(x, ids, z, x, weights=w, loss=gap(0, 62, n))
