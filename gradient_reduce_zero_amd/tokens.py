@@ -29,9 +29,9 @@ _F32, _I32 = torch.float32, torch.int32
 # The smallest calls take a few microseconds on the device, about what the host
 # needs for one launch, so the checks below use the cheapest accessors: device
 # indices (-1 for the host) instead of device objects, and explanations only
-# where a check has failed.
-_current_gpu = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+# where a check has failed.  A torch without GPU support lacks the accessors of
+# _C that _call uses, so they are looked up there.
+_C = torch._C
 
 
 def _device(t, name, dev=None):
@@ -100,13 +100,13 @@ def _call(name, dev, stream, *args):
     """Call entry point ``name`` with GPU ``dev`` current, on ``stream`` or its
     current stream."""
     if stream is None:
-        handle = _current_stream(dev)
+        handle = _C._cuda_getCurrentRawStream(dev)
     elif stream.device.index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
     else:
         handle = stream.cuda_stream
     fn = getattr(lib(), name)
-    if _current_gpu() == dev:
+    if _C._cuda_getDevice() == dev:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
