@@ -7,7 +7,9 @@ import pytest
 import torch
 
 import gradient_reduce_zero_amd as grz
-from test_gpu_tokens import BF16, DEV, F32, logits_of, logprob_call, order_of
+import token_ref as ref
+from test_gpu_tokens import (BF16, DEV, F32, grad_call, logits_of, logprob_call, matrix, order_of,
+                             outside_untouched)
 
 pytestmark = pytest.mark.gpu
 
@@ -94,3 +96,46 @@ def test_arrays_between_the_rows_of_the_logits():
         assert torch.equal(got, one)
     with pytest.raises(grz.GrzError):  # one place further it reaches the next row
         grz.dp_distill_grad(x, ids, z, x, weights=w, loss=gap(0, 62, n))
+
+
+@pytest.mark.parametrize("n", [32769, 65536, 65537, 262145])
+@pytest.mark.parametrize("vocab", [262143, 262144, 300000])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad_of_many_ids_into_large_tables(n, vocab, accumulate):
+    # On both sides of where the ids' digits take a third pass of the sort, and of
+    # where its tiles grow and their counts are summed by a launch of their own.
+    dim = 4
+    g = torch.Generator(device=DEV).manual_seed(90)
+    ids = torch.randint(-1, vocab, (n,), device=DEV, generator=g)
+    ids[torch.rand(n, device=DEV, generator=g) < 0.2] = vocab - 1
+    ids[n // 2] = 0
+    ids[n // 3] = vocab
+    dout, _ = matrix(n, dim, F32, seed=91)
+    table, buf = matrix(vocab, dim, F32, seed=92, pad=4, shift=4)
+    before, old = buf.clone(), table.clone()
+    grad_call(dout, ids, table, scale=0.5, accumulate=accumulate)
+    want, tol = ref.embed_grad(dout, ids, vocab, 0.5, old if accumulate else None)
+    ref.assert_close(table, want, tol, "dtable")
+    assert outside_untouched(table, buf, before)
+    again = old.clone()
+    grad_call(dout, ids.int(), again, scale=0.5, accumulate=accumulate)
+    ref.assert_close(again, want, tol, "int32 ids")
+
+
+@pytest.mark.parametrize("n", [3, 4097, 40000])
+def test_embed_grad_into_the_largest_table(n):
+    # 2^26 rows, the most that are taken: keys of 27 bits.
+    vocab = 2 ** 26
+    g = torch.Generator(device=DEV).manual_seed(93)
+    ids = torch.randint(0, vocab, (n,), device=DEV, generator=g)
+    ids[0], ids[-1], ids[n // 2] = vocab - 1, 0, vocab
+    dout, _ = matrix(n, 1, F32, seed=94)
+    table = torch.full((vocab, 1), 7.0, device=DEV)
+    grad_call(dout, ids, table)
+    named, place = torch.unique(ids[ids < vocab], return_inverse=True)
+    small = torch.full_like(ids, -1)
+    small[ids < vocab] = place
+    want, tol = ref.embed_grad(dout, small, len(named), 1.0)
+    ref.assert_close(table[named], want, tol, "named rows")
+    table[named] = 0.0
+    assert (table == 0).all()
