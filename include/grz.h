@@ -104,8 +104,8 @@ enum { GRZ_F32 = 0, GRZ_BF16 = 1, GRZ_F64 = 2 };
  * GRZ_SUM; zero1_adamw_gather takes GRZ_UNEVEN, GRZ_ARGS_DEVICE and
  * GRZ_MEAN_BF16; the
  * all-gathers take GRZ_UNEVEN; zero1_fused_step GRZ_UNEVEN, GRZ_IN_COMPACT,
- * GRZ_ARGS_DEVICE and GRZ_COOPERATIVE; dp_embed_grad GRZ_ACCUMULATE.  Their meaning is in each entry
- * point's comment. */
+ * GRZ_ARGS_DEVICE and GRZ_COOPERATIVE; dp_embed_grad GRZ_ACCUMULATE.  Their
+ * meaning is in each entry point's comment. */
 enum {
   GRZ_SUM = 1,        /* keep the sum: skip the division by N            */
   GRZ_UNEVEN = 2,     /* allow bucket lengths not divisible by N         */
@@ -632,7 +632,9 @@ int dp_embed_grad(const void* dout, int dout_dtype, int64_t dout_stride, const v
  * top_logprobs  device fp32[n * top]: their log q.
  * A logit of -inf is a token of probability 0.  A row that holds a NaN or
  * +inf, or nothing but -inf, has no softmax: its results are NaN (its top ids
- * are still in order).
+ * are still in order).  The top list of such a row, of one with fewer logits above
+ * -inf than top, or with several hundred near the top-th largest, may take a pass
+ * over the row per place.
  * Errors: GRZ_EINVAL also when no output is asked for.
  */
 int dp_token_logprobs(const void* logits, int dtype, int64_t n, int64_t vocab, int64_t stride,
