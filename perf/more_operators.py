@@ -228,7 +228,7 @@ def _run_own(s):
         grz.dp_expert_route_grad(s["x"], s["ids"], s["dweights"], s["dx"],
                                  normalize=s["normalize"])
         return {"dlogits": s["dx"]}
-    w = s["weights"] if s.get("weighted", True) else None
+    w = s.get("weights") if s.get("weighted", True) else None
     if op == "dispatch":
         grz.dp_expert_sort(s["ids_in"], s["experts"], s["offsets"], s["places"], s["ws"])
         grz.dp_expert_dispatch(s["x"], s["places"], s["y"], weights=w)
