@@ -17,11 +17,13 @@ GRZ_OK, GRZ_EINVAL, GRZ_EINDIVISIBLE, GRZ_EALIGN, GRZ_EHIP, GRZ_ERANGE = range(6
 GRZ_F32, GRZ_BF16, GRZ_F64 = 0, 1, 2
 (GRZ_SUM, GRZ_UNEVEN, GRZ_IN_COMPACT, GRZ_BF16_WIRE, GRZ_IN_RANGE, GRZ_ARGS_DEVICE,
  GRZ_OUT_GLOBAL, GRZ_IN_TILED, GRZ_MEAN_BF16, GRZ_COOPERATIVE,
- GRZ_ACCUMULATE) = (1, 2, 4, 8, 16, 32, 64, 128, 256, 512, 1024)
+ GRZ_ACCUMULATE, GRZ_NORMALIZE) = (1, 2, 4, 8, 16, 32, 64, 128, 256, 512, 1024, 2048)
 GRZ_MAX_RANKS = 16
 GRZ_PIECE = 4096
 GRZ_NOALLOC_SCRATCH_BYTES = 65536
 GRZ_MAX_TOP = 128
+GRZ_MAX_EXPERTS = 1024
+GRZ_MAX_SLOTS = 32
 
 # Every symbol include/grz.h declares, with (restype, argtypes).
 _vp, _i, _i64, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_double
@@ -38,7 +40,12 @@ class AdamWArgs(ctypes.Structure):
                 ("lr", "beta1", "beta2", "eps", "weight_decay", "bias_corr1", "bias_corr2")]
 
 
+class Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
 _BP = ctypes.POINTER(Bucket)
+_TP = ctypes.POINTER(Tensor)
 SIGNATURES = {
     "grz_version": (_i, []),
     "grz_strerror": (ctypes.c_char_p, [_i]),
@@ -85,6 +92,20 @@ SIGNATURES = {
                              _vp]),
     "dp_distill_grad": (_i, [_vp, _i, _i64, _i64, _i64, _vp, _i, _vp, _i, _i, _f, _vp, _f, _vp,
                              _vp, _i64, _vp]),
+    "dp_expert_route": (_i, [_vp, _i, _i64, _i64, _i64, _i, _i, _vp, _vp, _vp]),
+    "dp_expert_route_grad": (_i, [_vp, _i, _i64, _i64, _i64, _i, _i, _vp, _vp, _vp, _i64, _vp]),
+    "dp_expert_sort_workspace": (ctypes.c_size_t, [_i64, _i, _i64]),
+    "dp_expert_sort": (_i, [_vp, _i, _i64, _i, _i64, _vp, _vp, _vp, _vp]),
+    "dp_expert_dispatch": (_i, [_vp, _i, _i64, _vp, _vp, _i64, _i, _i64, _i64, _vp, _i, _i64,
+                                _vp]),
+    "dp_expert_combine": (_i, [_vp, _i, _i64, _i64, _vp, _vp, _i64, _i, _i64, _i, _vp, _i, _i64,
+                               _vp]),
+    "dp_expert_combine_grad": (_i, [_vp, _i, _i64, _vp, _i, _i64, _i64, _vp, _vp, _i64, _i, _i64,
+                                    _vp, _i64, _vp, _vp]),
+    "dp_tensor_pieces": (_i64, [_TP, _i64]),
+    "dp_grad_sqnorm_tensors_workspace": (ctypes.c_size_t, [_TP, _i64, _i64]),
+    "dp_grad_sqnorm_tensors": (_i, [_TP, _i64, _d, _i64, _vp, _vp, _vp, _vp]),
+    "dp_grad_clip_tensors": (_i, [_TP, _i64, _vp, _TP, _vp]),
 }
 
 _lib = None

@@ -16,7 +16,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "grz.hip")
 TOKENS_SRC = os.path.join(HERE, "csrc", "tokens.hip")
-SRCS = (SRC, TOKENS_SRC)
+EXPERTS_SRC = os.path.join(HERE, "csrc", "experts.hip")
+TENSORS_SRC = os.path.join(HERE, "csrc", "tensors.hip")
+SRCS = (SRC, TOKENS_SRC, EXPERTS_SRC, TENSORS_SRC)
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgrz.so")
 ARCH = "gfx950"

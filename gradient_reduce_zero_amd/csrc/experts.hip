@@ -1,0 +1,998 @@
+// experts.hip -- HIP kernels and C ABI of the mixture-of-experts operators for AMD
+// Instinct MI355X (gfx950, CDNA4, wave64):
+//   dp_expert_route         a token's experts and their weights from its logits
+//   dp_expert_route_grad    the gradient of the weights, to the logits
+//   dp_expert_sort          places of the tokens' slots sorted by expert
+//   dp_expert_dispatch      tokens' rows to those places
+//   dp_expert_combine       rows back, summed with the weights (and the gradient
+//                           of the dispatch)
+//   dp_expert_combine_grad  gradient of that sum: to the rows and to the weights
+//
+// All are bound by HBM or, where small, by their launches: at most three flops
+// per byte.  Integer atomics in LDS only, so every result bit is the same from run
+// to run.
+
+#include <hip/hip_runtime.h>
+
+#include <limits.h>
+#include <stdint.h>
+
+#include "grz.h"
+#include "rows.h"
+
+namespace {
+
+constexpr int64_t kSlots = int64_t{1} << 28;      // n * k of one call
+constexpr int64_t kCols = int64_t{65535} * 64;    // columns: 2^16 column blocks of a launch
+constexpr int64_t kTokenBatch = int64_t{1} << 21;  // tokens of one launch
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// ---------------------------------------------------------------------------
+// Vectors of a row that begin anywhere: gfx950 reads and writes 8 and 16 bytes at
+// any element's address, so rows need no alignment of their own.
+
+template <typename T, int N>
+__device__ __forceinline__ void load_cols(const T* p, float (&x)[N]) {
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (N == 8) {
+      const u32x4e u = *reinterpret_cast<const u32x4e*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
+    } else {
+      static_assert(N == 4, "bf16 vectors hold 4 or 8 elements");
+      const u32x2e u = *reinterpret_cast<const u32x2e*>(p);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
+    }
+  } else {
+    static_assert(N == 4, "fp32 vectors hold 4 elements");
+    const u32x4e u = *reinterpret_cast<const u32x4e*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]);
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_cols(T* p, const float (&x)[N]) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t u[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      u[i] = bf16_bits(x[2 * i]) | (bf16_bits(x[2 * i + 1]) << 16);
+    if constexpr (N == 8)
+      __builtin_nontemporal_store(u32x4e{u[0], u[1], u[2], u[3]}, reinterpret_cast<u32x4e*>(p));
+    else
+      __builtin_nontemporal_store(u32x2e{u[0], u[1]}, reinterpret_cast<u32x2e*>(p));
+  } else {
+    __builtin_nontemporal_store(u32x4e{__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                       __float_as_uint(x[2]), __float_as_uint(x[3])},
+                                reinterpret_cast<u32x4e*>(p));
+  }
+}
+
+// Columns of a lane's vector: 16 bytes, of fp32 if one of the types is.
+template <typename A, typename B> constexpr int cols_of() {
+  return sizeof(A) == 2 && sizeof(B) == 2 ? 8 : 4;
+}
+
+__device__ __forceinline__ int wave_index() {
+  return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
+// ---------------------------------------------------------------------------
+// The router.  A row of up to 1024 logits stays in the registers of G lanes (16,
+// four rows to a wave, or 64), V consecutive ones in each, so that every maximum
+// and sum is V operations and four (or six) lane exchanges.  The k largest come
+// one at a time: the row's largest key, the lowest lane that holds it, its lowest
+// element, which is then taken out.
+
+// Keys ordered as the logits are: larger for larger, NaN above all, -0 as 0, and 0
+// for an element that is not there or taken out.
+constexpr uint32_t kClosed = 0x007fffffu;  // the key of -inf
+constexpr uint32_t kNanKey = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  const uint32_t key = b & 0x80000000u ? ~b : b | 0x80000000u;
+  return x != x ? kNanKey : key;
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+template <int CTRL> __device__ __forceinline__ uint32_t lane_swap_bits(uint32_t v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
+}
+
+template <int G> __device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  v = max(v, lane_swap_bits<kSwap1>(v));
+  v = max(v, lane_swap_bits<kSwap2>(v));
+  v = max(v, lane_swap_bits<kHalfMirror>(v));
+  v = max(v, lane_swap_bits<kMirror>(v));
+  if constexpr (G == 64) {
+    auto row = [&](int lane) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(v, lane)); };
+    v = max(max(row(0), row(16)), max(row(32), row(48)));
+  }
+  return v;
+}
+template <int G> __device__ __forceinline__ float group_max(float v) {
+  if constexpr (G == 64) return wave_max(v);
+  v = fmaxf(v, lane_swap<kSwap1>(v));
+  v = fmaxf(v, lane_swap<kSwap2>(v));
+  v = fmaxf(v, lane_swap<kHalfMirror>(v));
+  return fmaxf(v, lane_swap<kMirror>(v));
+}
+template <int G> __device__ __forceinline__ float group_sum(float v) {
+  if constexpr (G == 64) return wave_sum(v);
+  v += lane_swap<kSwap1>(v);
+  v += lane_swap<kSwap2>(v);
+  v += lane_swap<kHalfMirror>(v);
+  return v + lane_swap<kMirror>(v);
+}
+// The lanes of the thread's group for which `yes` holds, the group's first at bit 0.
+template <int G> __device__ __forceinline__ uint64_t group_ballot(bool yes) {
+  const uint64_t b = __ballot(yes);
+  if constexpr (G == 64) return b;
+  return (b >> (threadIdx.x & 48)) & 0xffffu;
+}
+
+// e^(x - m) of an open expert, 0 of a closed one; one rounding each of the
+// difference and its product.
+__device__ __forceinline__ float weight_of(float x, float m) {
+  return x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((x - m) * kLog2e);
+}
+
+// The row's logits V * g .. V * g + V - 1, -inf behind the last.
+template <typename T, int V>
+__device__ __forceinline__ void load_logits(const T* row, int experts, int g, bool live,
+                                            float (&x)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = -INFINITY;
+  if (!live) return;
+  constexpr int E = sizeof(T) == 2 && V >= 8 ? 8 : 4;
+  const int c = g * V;
+  if (V >= 4 && c + V <= experts) {
+    if constexpr (V >= 4) {
+#pragma unroll
+      for (int h = 0; h < V / E; ++h) {
+        float y[E];
+        load_cols<T, E>(row + c + h * E, y);
+#pragma unroll
+        for (int i = 0; i < E; ++i) x[h * E + i] = y[i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c + i < experts) x[i] = widen(row[c + i]);
+  }
+}
+
+template <typename T, int G, int V>
+__global__ __launch_bounds__(256) void route_kernel(const T* __restrict__ logits, int64_t stride,
+                                                    int64_t row0, int64_t n, int experts, int k,
+                                                    bool normalize, int32_t* __restrict__ ids,
+                                                    float* __restrict__ weights) {
+  const int g = threadIdx.x & (G - 1);
+  const int64_t row = row0 + static_cast<int64_t>(blockIdx.x) * (256 / G) + threadIdx.x / G;
+  const bool live = row < n;
+  float x[V];
+  load_logits<T, V>(logits + (live ? row : 0) * stride, experts, g, live, x);
+  uint32_t key[V], best = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    key[i] = live && g * V + i < experts ? key_of(x[i]) : 0u;
+    best = max(best, key[i]);
+  }
+  uint32_t top = group_max<G>(best);
+  const bool open = top > kClosed;
+  const float m = value_of(top);
+  float total = 0.0f;
+  if (!normalize) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) total += weight_of(x[i], m);
+    total = group_sum<G>(total);
+  }
+  int id = -1;
+  float e = 0.0f;  // of the slot that the thread stores
+  for (int j = 0; j < k; ++j) {
+    if (j > 0) {
+      best = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) best = max(best, key[i]);
+      top = group_max<G>(best);
+    }
+    const uint64_t who = group_ballot<G>(best == top);
+    const int owner = __builtin_ctzll(who | (1ull << 63));
+    int at = 0;
+    if (g == owner) {
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const bool hit = key[i] == top && !found;
+        at = hit ? i : at;
+        key[i] = hit ? 0u : key[i];
+        found = found || hit;
+      }
+    }
+    at = __shfl(at, owner, G);
+    const float p = top > kClosed ? weight_of(value_of(top), m) : 0.0f;
+    if (normalize) total += p;
+    if (g == j) {
+      id = top > kClosed ? owner * V + at : -1;
+      e = p;
+    }
+  }
+  if (live && g < k) {
+    ids[row * k + g] = id;
+    weights[row * k + g] = open ? e / total : 0.0f;
+  }
+}
+
+// Lane j of a row's group takes slot j.  The slots' shares meet the row through
+// LDS, where each lane finds those of its elements; a token that lists an expert
+// twice has both slots add theirs up first, in the slots' order.
+template <typename T, int G, int V>
+__global__ __launch_bounds__(256) void route_grad_kernel(
+    const T* logits, int64_t stride, int64_t row0, int64_t n, int experts, int k, bool normalize,
+    const int32_t* __restrict__ ids, const float* __restrict__ dweights, T* dlogits,
+    int64_t dstride) {
+  __shared__ float shares[256 / G][G * V];
+  const int g = threadIdx.x & (G - 1);
+  const int64_t row = row0 + static_cast<int64_t>(blockIdx.x) * (256 / G) + threadIdx.x / G;
+  const bool live = row < n;
+  const T* src = logits + (live ? row : 0) * stride;
+  float* mine = shares[threadIdx.x / G];
+  int id = -1;
+  float dw = 0.0f, xj = -INFINITY;
+  if (live && g < k) {
+    id = ids[row * k + g];
+    if (id < 0 || id >= experts) id = -1;
+    if (id >= 0) {
+      dw = dweights[row * k + g];
+      xj = widen(src[id]);
+    }
+  }
+  float x[V], m, total = 0.0f, ej;
+  if (normalize) {
+    m = group_max<G>(xj);
+    ej = weight_of(xj, m);
+    total = group_sum<G>(ej);
+  } else {
+    load_logits<T, V>(src, experts, g, live, x);
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, x[i]);
+    m = group_max<G>(m);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      x[i] = weight_of(x[i], m);
+      total += x[i];
+    }
+    total = group_sum<G>(total);
+    ej = weight_of(xj, m);
+  }
+  const float w = total == 0.0f ? 0.0f : ej / total;
+  const float both = group_sum<G>(id >= 0 ? dw * w : 0.0f);
+  const float share = id < 0 ? 0.0f : w * (normalize ? dw - both : dw);
+  const bool some = group_ballot<G>(id >= 0 && dw != 0.0f) != 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) mine[g * V + i] = 0.0f;
+  float sum = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    const int other = __shfl(id, j, G);
+    const float s = __shfl(share, j, G);
+    if (other == id) sum += s;
+  }
+  wave_fence();
+  if (id >= 0) mine[id] = sum;  // equal ids store the same sum
+  wave_fence();
+  if (!live) return;
+  T* dst = dlogits + row * dstride;
+  float d[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    d[i] = mine[g * V + i];
+    if (!normalize) d[i] -= total == 0.0f ? 0.0f : both * (x[i] / total);
+    if (!some) d[i] = 0.0f;
+  }
+  constexpr int E = sizeof(T) == 2 && V >= 8 ? 8 : 4;
+  const int c = g * V;
+  if (V >= 4 && c + V <= experts) {
+    if constexpr (V >= 4) {
+#pragma unroll
+      for (int h = 0; h < V / E; ++h) {
+        float y[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) y[i] = d[h * E + i];
+        store_cols<T, E>(dst + c + h * E, y);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c + i < experts) put(dst + c + i, d[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The sort of the slots by expert: stable, so a place is the number of slots of
+// lower experts, plus the slots of the same expert before it.  A workgroup places
+// a tile of slots, 1024 at a time: the ballots of the id's bits give a slot's
+// place among the equal ones of its wave, counts in LDS those of the waves before
+// it, and `before` those of the tiles before its own.
+//
+//  - up to kDirectSlots one launch: each workgroup counts all slots itself, those
+//    before its tile and all, with integer atomics in LDS;
+//  - beyond that the tiles are counted by a first launch, at most kMaxTiles of
+//    them, and each workgroup adds their counts up.
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int64_t kDirectSlots = 16384;
+constexpr int64_t kMaxTiles = 256;
+
+struct SortArgs {
+  const void* ids;
+  int id_bits;
+  int64_t slots;
+  int experts;
+  int bits;       // of `experts`
+  int64_t tile;   // slots of a tile, a multiple of kSortThreads
+  int tiles;
+  uint32_t* counts;  // [tiles][experts]
+  int32_t* offsets;
+  int32_t* places;
+};
+
+// The slot's expert, `experts` for none.
+__device__ __forceinline__ int expert_at(const SortArgs& a, int64_t i) {
+  const int64_t id = id_at(a.ids, a.id_bits, i);
+  return id >= 0 && id < a.experts ? static_cast<int>(id) : a.experts;
+}
+
+__global__ __launch_bounds__(kSortThreads) void expert_count_kernel(SortArgs a) {
+  __shared__ uint32_t count[GRZ_MAX_EXPERTS];
+  if (threadIdx.x < a.experts) count[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t from = blockIdx.x * a.tile;
+  const int64_t to = from + a.tile < a.slots ? from + a.tile : a.slots;
+  for (int64_t i = from + threadIdx.x; i < to; i += kSortThreads) {
+    const int e = expert_at(a, i);
+    if (e < a.experts) atomicAdd(&count[e], 1u);
+  }
+  __syncthreads();
+  if (threadIdx.x < a.experts)
+    a.counts[static_cast<int64_t>(blockIdx.x) * a.experts + threadIdx.x] = count[threadIdx.x];
+}
+
+template <bool DIRECT>
+__global__ __launch_bounds__(kSortThreads) void expert_place_kernel(SortArgs a) {
+  __shared__ uint32_t before[GRZ_MAX_EXPERTS], total[GRZ_MAX_EXPERTS];
+  __shared__ uint32_t sums[kSortWaves];
+  extern __shared__ uint16_t in_wave[];  // [kSortWaves][experts]
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, experts = a.experts;
+  const int64_t from = blockIdx.x * a.tile;
+  const int64_t to = from + a.tile < a.slots ? from + a.tile : a.slots;
+  if (tid < experts) before[tid] = total[tid] = 0;
+  __syncthreads();
+  if constexpr (DIRECT) {
+#pragma unroll 4
+    for (int64_t i = tid; i < a.slots; i += kSortThreads) {
+      const int e = expert_at(a, i);
+      if (e < experts) {
+        atomicAdd(&total[e], 1u);
+        if (i < from) atomicAdd(&before[e], 1u);
+      }
+    }
+  } else {
+    const int parts = kSortThreads / experts, e = tid % experts, part = tid / experts;
+    if (part < parts) {
+      uint32_t b = 0, t = 0;
+#pragma unroll 8
+      for (int k = part; k < a.tiles; k += parts) {
+        const uint32_t c = a.counts[static_cast<int64_t>(k) * experts + e];
+        t += c;
+        b += k < static_cast<int>(blockIdx.x) ? c : 0u;
+      }
+      atomicAdd(&before[e], b);
+      atomicAdd(&total[e], t);
+    }
+  }
+  __syncthreads();
+  // The experts' first rows: an exclusive scan of their totals.
+  const uint32_t own = tid < experts ? total[tid] : 0u;
+  uint32_t scan = own;
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const uint32_t v = __shfl_up(scan, s, 64);
+    if (lane >= s) scan += v;
+  }
+  if (lane == 63) sums[wave] = scan;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) scan += sums[w];
+  if (tid < experts) {
+    before[tid] += scan - own;
+    if (blockIdx.x == 0) {
+      a.offsets[tid] = static_cast<int32_t>(scan - own);
+      if (tid == experts - 1) a.offsets[experts] = static_cast<int32_t>(scan);
+    }
+  }
+  for (int64_t base = from; base < to; base += kSortThreads) {
+    const int64_t i = base + tid;
+    const int e = i < to ? expert_at(a, i) : experts;
+    uint16_t* counts = in_wave + wave * experts;
+    for (int c = lane; c < experts; c += 64) counts[c] = 0;
+    uint64_t same = ~0ull;
+    for (int b = 0; b < a.bits; ++b) {
+      const uint64_t v = __ballot((e >> b) & 1);
+      same &= (e >> b) & 1 ? v : ~v;
+    }
+    const uint32_t rank = static_cast<uint32_t>(__popcll(same & ((1ull << lane) - 1)));
+    wave_fence();
+    if (e < experts && rank == 0) counts[e] = static_cast<uint16_t>(__popcll(same));
+    __syncthreads();
+    uint32_t run = 0;
+    if (tid < experts) {
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) {
+        const uint32_t c = in_wave[w * experts + tid];
+        in_wave[w * experts + tid] = static_cast<uint16_t>(run);
+        run += c;
+      }
+    }
+    __syncthreads();
+    if (i < to)
+      a.places[i] = e < experts ? static_cast<int32_t>(before[e] + counts[e] + rank) : -1;
+    __syncthreads();
+    if (tid < experts) before[tid] += run;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows to their places and back: a wave takes a token and a run of its columns,
+// its lanes 16-byte vectors along them; a token's places are the wave's, so they
+// sit in scalar registers.  The columns behind the last whole vector are taken one
+// by one by the waves of the last run.
+
+// out[places[i][j]] = (weights[i][j]) x[i]: the row is read once and stored k times.
+template <typename TI, typename TO, int U>
+__global__ __launch_bounds__(256) void dispatch_kernel(
+    const TI* __restrict__ x, int64_t xstride, const int32_t* __restrict__ places,
+    const float* __restrict__ weights, int64_t row0, int64_t n, int k, int64_t dim, int64_t rows,
+    TO* __restrict__ out, int64_t ostride) {
+  constexpr int VEC = cols_of<TI, TO>();
+  const int lane = threadIdx.x & 63;
+  const int64_t token = row0 + static_cast<int64_t>(blockIdx.x) * 4 + wave_index();
+  if (token >= n) return;
+  const TI* src = x + token * xstride;
+  const int64_t whole = dim - dim % VEC;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (64 * VEC * U) + lane * VEC;
+  float v[U][VEC], last = 0.0f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t c = c0 + u * 64 * VEC;
+    if (c < whole) load_cols<TI, VEC>(src + c, v[u]);
+  }
+  const bool tail = blockIdx.y == gridDim.y - 1 && lane < dim - whole;
+  if (tail) last = widen(src[whole + lane]);
+  for (int j = 0; j < k; ++j) {
+    const int64_t p = places[token * k + j];
+    if (p < 0 || p >= rows) continue;
+    const float w = weights != nullptr ? weights[token * k + j] : 1.0f;
+    TO* dst = out + p * ostride;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = c0 + u * 64 * VEC;
+      if (c >= whole) continue;
+      float y[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) y[i] = v[u][i] * w;
+      store_cols<TO, VEC>(dst + c, y);
+    }
+    if (tail) put(dst + whole + lane, last * w);
+  }
+}
+
+// out[i] = sum over j of (weights[i][j]) y[places[i][j]], added to out[i] with ACC:
+// KB rows' vectors on their way at once, summed in the slots' order.
+template <typename TI, typename TO, int U, int KB, bool ACC>
+__global__ __launch_bounds__(256) void combine_kernel(
+    const TI* __restrict__ y, int64_t ystride, int64_t rows, const int32_t* __restrict__ places,
+    const float* __restrict__ weights, int64_t row0, int64_t n, int k, int64_t dim,
+    TO* __restrict__ out, int64_t ostride) {
+  constexpr int VEC = cols_of<TI, TO>();
+  const int lane = threadIdx.x & 63;
+  const int64_t token = row0 + static_cast<int64_t>(blockIdx.x) * 4 + wave_index();
+  if (token >= n) return;
+  TO* dst = out + token * ostride;
+  const int64_t whole = dim - dim % VEC;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (64 * VEC * U) + lane * VEC;
+  const bool tail = blockIdx.y == gridDim.y - 1 && lane < dim - whole;
+  float acc[U][VEC], last = 0.0f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[u][i] = 0.0f;
+    const int64_t c = c0 + u * 64 * VEC;
+    if (ACC && c < whole) load_cols<TO, VEC>(dst + c, acc[u]);
+  }
+  if (ACC && tail) last = widen(dst[whole + lane]);
+  for (int j0 = 0; j0 < k; j0 += KB) {
+    float v[KB][U][VEC], w[KB];
+    int64_t p[KB];
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      p[b] = j0 + b < k ? places[token * k + j0 + b] : -1;
+      if (p[b] >= rows) p[b] = -1;
+      w[b] = weights != nullptr && p[b] >= 0 ? weights[token * k + j0 + b] : 1.0f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[b][u][i] = 0.0f;
+        const int64_t c = c0 + u * 64 * VEC;
+        if (p[b] >= 0 && c < whole) load_cols<TI, VEC>(y + p[b] * ystride + c, v[b][u]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      if (p[b] < 0) continue;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[u][i] = fmaf(v[b][u][i], w[b], acc[u][i]);
+      if (tail) last = fmaf(widen(y[p[b] * ystride + whole + lane]), w[b], last);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t c = c0 + u * 64 * VEC;
+    if (c < whole) store_cols<TO, VEC>(dst + c, acc[u]);
+  }
+  if (tail) put(dst + whole + lane, last);
+}
+
+// dy[places[i][j]] = weights[i][j] dout[i] and dweights[i][j] = <dout[i],
+// y[places[i][j]]>: W waves to a token, each with every W-th run of columns; the
+// rows' products are summed over the lanes, then over the waves.  dy may be y: a
+// lane stores where it has read.
+template <typename TD, typename TY, int U, int KB, int W>
+__global__ __launch_bounds__(256) void combine_grad_kernel(
+    const TD* __restrict__ dout, int64_t dstride, const TY* y, int64_t ystride, int64_t rows,
+    const int32_t* __restrict__ places, const float* __restrict__ weights, int64_t row0,
+    int64_t n, int k, int64_t dim, TY* dy, int64_t dystride, float* __restrict__ dweights) {
+  constexpr int VEC = cols_of<TD, TY>();
+  __shared__ float part[4][KB];
+  const int lane = threadIdx.x & 63, wave = wave_index();
+  const int64_t token = row0 + static_cast<int64_t>(blockIdx.x) * (4 / W) + wave / W;
+  if (token >= n) return;  // W = 4: the whole workgroup
+  const TD* src = dout + token * dstride;
+  const int64_t whole = dim - dim % VEC;
+  const bool tail = wave % W == 0 && lane < dim - whole;
+  for (int j0 = 0; j0 < k; j0 += KB) {
+    float w[KB], dot[KB];
+    int64_t p[KB];
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      p[b] = j0 + b < k ? places[token * k + j0 + b] : -1;
+      if (p[b] >= rows) p[b] = -1;
+      w[b] = weights != nullptr && p[b] >= 0 ? weights[token * k + j0 + b] : 1.0f;
+      dot[b] = 0.0f;
+    }
+    for (int64_t c0 = (wave % W) * (64 * VEC * U) + lane * VEC; c0 < whole;
+         c0 += W * 64 * VEC * U) {
+      float d[U][VEC], v[KB][U][VEC];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t c = c0 + u * 64 * VEC;
+        if (c < whole) load_cols<TD, VEC>(src + c, d[u]);
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+          if (p[b] >= 0 && dweights != nullptr && c < whole)
+            load_cols<TY, VEC>(y + p[b] * ystride + c, v[b][u]);
+      }
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        if (p[b] < 0) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t c = c0 + u * 64 * VEC;
+          if (c >= whole) continue;
+          if (dweights != nullptr) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) dot[b] = fmaf(d[u][i], v[b][u][i], dot[b]);
+          }
+          if (dy != nullptr) {
+            float o[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] = d[u][i] * w[b];
+            store_cols<TY, VEC>(dy + p[b] * dystride + c, o);
+          }
+        }
+      }
+    }
+    if (tail) {
+      const float d = widen(src[whole + lane]);
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        if (p[b] < 0) continue;
+        if (dweights != nullptr)
+          dot[b] = fmaf(d, widen(y[p[b] * ystride + whole + lane]), dot[b]);
+        if (dy != nullptr) put(dy + p[b] * dystride + whole + lane, d * w[b]);
+      }
+    }
+    if (dweights == nullptr) continue;
+#pragma unroll
+    for (int b = 0; b < KB; ++b) dot[b] = wave_sum(dot[b]);
+    if constexpr (W > 1) {
+      if (lane == 0) {
+#pragma unroll
+        for (int b = 0; b < KB; ++b) part[wave][b] = dot[b];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+        dot[b] = (part[0][b] + part[1][b]) + (part[2][b] + part[3][b]);
+      __syncthreads();
+    }
+    if (wave % W == 0) {
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+        if (lane == b && j0 + b < k)
+          dweights[token * k + j0 + b] = p[b] < 0 ? 0.0f : dot[b];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+// n x k arrays of 4-byte values.
+int check_slots(const void* p, int64_t n, int k, bool may_be_null = false) {
+  if (n == 0) return GRZ_OK;
+  if (p == nullptr) return may_be_null ? GRZ_OK : GRZ_EINVAL;
+  return aligned(p, 4) ? GRZ_OK : GRZ_EALIGN;
+}
+int check_counts(int64_t n, int k) {
+  if (n < 0 || k < 1 || k > GRZ_MAX_SLOTS) return GRZ_EINVAL;
+  return n > kSlots / k ? GRZ_ERANGE : GRZ_OK;
+}
+
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+Span slot_span(const void* p, int64_t n, int k) {
+  return {p, p != nullptr ? static_cast<size_t>(n) * k * 4 : 0};
+}
+Span matrix_span(const void* p, int dtype, int64_t rows, int64_t cols, int64_t stride) {
+  return {p, p != nullptr ? span_of(dtype, rows, cols, stride) : 0};
+}
+// Whether an output lies over one of the other arrays.
+template <int N> bool clash(const Span& out, const Span (&others)[N]) {
+  for (const Span& s : others)
+    if (overlap(out.at, out.bytes, s.at, s.bytes)) return true;
+  return false;
+}
+
+// f(rows of the batch, first row) over at most `batch` tokens at a time.
+template <typename F> int in_batches(int64_t n, int64_t batch, F f) {
+  for (int64_t r = 0; r < n; r += batch) {
+    const int st = f(n - r < batch ? n - r : batch, r);
+    if (st != GRZ_OK) return st;
+  }
+  return GRZ_OK;
+}
+
+// Lanes to a row and logits to a lane.  Sixteen lanes up to 256 experts and 16
+// slots: four rows share a wave's instructions.
+#define GRZ_ROUTE_SHAPES(CALL)               \
+  if (k <= 16 && experts <= 16) CALL(16, 1)  \
+  if (k <= 16 && experts <= 64) CALL(16, 4)  \
+  if (k <= 16 && experts <= 128) CALL(16, 8) \
+  if (k <= 16 && experts <= 256) CALL(16, 16) \
+  if (experts <= 256) CALL(64, 4)            \
+  CALL(64, 16)
+
+template <typename T>
+int route_run(const void* logits, int64_t n, int experts, int64_t stride, int k, bool normalize,
+              int32_t* ids, float* weights, hipStream_t stream) {
+#define GRZ_CALL(G, V)                                                                       \
+  return in_batches(n, kTokenBatch, [&](int64_t rows, int64_t r) {                           \
+    return launch(route_kernel<T, G, V>,                                                     \
+                  dim3(static_cast<unsigned>(ceil_div(rows, 256 / G))), dim3(256), stream,   \
+                  static_cast<const T*>(logits), stride, r, n, experts, k, normalize, ids,   \
+                  weights);                                                                  \
+  });
+  GRZ_ROUTE_SHAPES(GRZ_CALL)
+#undef GRZ_CALL
+}
+
+template <typename T>
+int route_grad_run(const void* logits, int64_t n, int experts, int64_t stride, int k,
+                   bool normalize, const int32_t* ids, const float* dweights, void* dlogits,
+                   int64_t dstride, hipStream_t stream) {
+#define GRZ_CALL(G, V)                                                                       \
+  return in_batches(n, kTokenBatch, [&](int64_t rows, int64_t r) {                           \
+    return launch(route_grad_kernel<T, G, V>,                                                \
+                  dim3(static_cast<unsigned>(ceil_div(rows, 256 / G))), dim3(256), stream,   \
+                  static_cast<const T*>(logits), stride, r, n, experts, k, normalize, ids,   \
+                  dweights, static_cast<T*>(dlogits), dstride);                              \
+  });
+  GRZ_ROUTE_SHAPES(GRZ_CALL)
+#undef GRZ_CALL
+}
+
+int check_route(const void* logits, int dtype, int64_t n, int64_t experts, int64_t stride, int k,
+                int flags) {
+  if (flags & ~GRZ_NORMALIZE) return GRZ_EINVAL;
+  if (experts < 1 || k > experts) return GRZ_EINVAL;
+  if (experts > GRZ_MAX_EXPERTS) return GRZ_ERANGE;
+  const int st = check_counts(n, k);
+  return st != GRZ_OK ? st : check_matrix(logits, dtype, n, experts, stride);
+}
+
+int64_t tile_of(int64_t slots) {
+  return slots <= kDirectSlots
+             ? kSortThreads
+             : ceil_div(slots, kMaxTiles * kSortThreads) * kSortThreads;
+}
+int bits_of(int v) {
+  int b = 1;
+  while (v >> b) ++b;
+  return b;
+}
+
+// Waves below which a call spreads its tokens' columns over more of them.
+constexpr int64_t kFewWaves = 4096;
+
+template <typename TI, typename TO>
+int dispatch_run(const void* x, int64_t xstride, const int32_t* places, const float* weights,
+                 int64_t n, int k, int64_t dim, int64_t rows, void* out, int64_t ostride,
+                 hipStream_t stream) {
+  constexpr int VEC = cols_of<TI, TO>();
+  const bool few = n * ceil_div(dim, 64 * VEC * 4) < kFewWaves;
+  const int64_t parts = ceil_div(dim, 64 * VEC * (few ? 1 : 4));
+  return in_batches(n, kTokenBatch, [&](int64_t tokens, int64_t r) {
+    return launch(few ? dispatch_kernel<TI, TO, 1> : dispatch_kernel<TI, TO, 4>,
+                  dim3(static_cast<unsigned>(ceil_div(tokens, 4)), static_cast<unsigned>(parts)),
+                  dim3(256), stream, static_cast<const TI*>(x), xstride, places, weights, r, n, k,
+                  dim, rows, static_cast<TO*>(out), ostride);
+  });
+}
+
+template <typename TI, typename TO, bool ACC>
+int combine_run(const void* y, int64_t ystride, int64_t rows, const int32_t* places,
+                const float* weights, int64_t n, int k, int64_t dim, void* out, int64_t ostride,
+                hipStream_t stream) {
+  constexpr int VEC = cols_of<TI, TO>();
+  auto go = [&](auto kernel, int u) {
+    const int64_t parts = ceil_div(dim, 64 * VEC * u);
+    return in_batches(n, kTokenBatch, [&](int64_t tokens, int64_t r) {
+      return launch(kernel,
+                    dim3(static_cast<unsigned>(ceil_div(tokens, 4)),
+                         static_cast<unsigned>(parts)),
+                    dim3(256), stream, static_cast<const TI*>(y), ystride, rows, places, weights,
+                    r, n, k, dim, static_cast<TO*>(out), ostride);
+    });
+  };
+  const bool few = n * ceil_div(dim, 64 * VEC * 4) < kFewWaves;
+  if (k <= 2) return few ? go(combine_kernel<TI, TO, 1, 2, ACC>, 1)
+                         : go(combine_kernel<TI, TO, 4, 2, ACC>, 4);
+  if (k <= 4) return few ? go(combine_kernel<TI, TO, 1, 4, ACC>, 1)
+                         : go(combine_kernel<TI, TO, 2, 4, ACC>, 2);
+  return go(combine_kernel<TI, TO, 1, 8, ACC>, 1);
+}
+
+template <typename TD, typename TY>
+int combine_grad_run(const void* dout, int64_t dstride, const void* y, int64_t ystride,
+                     int64_t rows, const int32_t* places, const float* weights, int64_t n, int k,
+                     int64_t dim, void* dy, int64_t dystride, float* dweights,
+                     hipStream_t stream) {
+  auto go = [&](auto kernel, int w) {
+    return in_batches(n, kTokenBatch, [&](int64_t tokens, int64_t r) {
+      return launch(kernel, dim3(static_cast<unsigned>(ceil_div(tokens, 4 / w))), dim3(256),
+                    stream, static_cast<const TD*>(dout), dstride, static_cast<const TY*>(y),
+                    ystride, rows, places, weights, r, n, k, dim, static_cast<TY*>(dy), dystride,
+                    dweights);
+    });
+  };
+  const bool few = n < kFewWaves;
+  if (k <= 2) return few ? go(combine_grad_kernel<TD, TY, 2, 2, 4>, 4)
+                         : go(combine_grad_kernel<TD, TY, 2, 2, 1>, 1);
+  if (k <= 4) return few ? go(combine_grad_kernel<TD, TY, 1, 4, 4>, 4)
+                         : go(combine_grad_kernel<TD, TY, 1, 4, 1>, 1);
+  return few ? go(combine_grad_kernel<TD, TY, 1, 8, 4>, 4)
+             : go(combine_grad_kernel<TD, TY, 1, 8, 1>, 1);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// C ABI
+
+extern "C" {
+
+int dp_expert_route(const void* logits, int dtype, int64_t n, int64_t experts, int64_t stride,
+                    int k, int flags, int32_t* ids, float* weights, hipStream_t stream) {
+  int st = check_route(logits, dtype, n, experts, stride, k, flags);
+  if (st != GRZ_OK) return st;
+  if ((st = check_slots(ids, n, k)) != GRZ_OK) return st;
+  if ((st = check_slots(weights, n, k)) != GRZ_OK) return st;
+  if (n == 0) return GRZ_OK;
+  const Span in = matrix_span(logits, dtype, n, experts, stride);
+  const Span i = slot_span(ids, n, k), w = slot_span(weights, n, k);
+  if (clash(i, {in, w}) || clash(w, {in})) return GRZ_EINVAL;
+  const bool norm = flags & GRZ_NORMALIZE;
+  const int e = static_cast<int>(experts);
+  return dtype == GRZ_BF16
+             ? route_run<uint16_t>(logits, n, e, stride, k, norm, ids, weights, stream)
+             : route_run<float>(logits, n, e, stride, k, norm, ids, weights, stream);
+}
+
+int dp_expert_route_grad(const void* logits, int dtype, int64_t n, int64_t experts,
+                         int64_t stride, int k, int flags, const int32_t* ids,
+                         const float* dweights, void* dlogits, int64_t dlogits_stride,
+                         hipStream_t stream) {
+  int st = check_route(logits, dtype, n, experts, stride, k, flags);
+  if (st != GRZ_OK) return st;
+  if ((st = check_slots(ids, n, k)) != GRZ_OK) return st;
+  if ((st = check_slots(dweights, n, k)) != GRZ_OK) return st;
+  if ((st = check_matrix(dlogits, dtype, n, experts, dlogits_stride)) != GRZ_OK) return st;
+  if (n == 0) return GRZ_OK;
+  const Span out = matrix_span(dlogits, dtype, n, experts, dlogits_stride);
+  if (clash(out, {slot_span(ids, n, k), slot_span(dweights, n, k)})) return GRZ_EINVAL;
+  if (!(logits == dlogits && stride == dlogits_stride) &&
+      clash(out, {matrix_span(logits, dtype, n, experts, stride)}))
+    return GRZ_EINVAL;
+  const bool norm = flags & GRZ_NORMALIZE;
+  const int e = static_cast<int>(experts);
+  return dtype == GRZ_BF16
+             ? route_grad_run<uint16_t>(logits, n, e, stride, k, norm, ids, dweights, dlogits,
+                                        dlogits_stride, stream)
+             : route_grad_run<float>(logits, n, e, stride, k, norm, ids, dweights, dlogits,
+                                     dlogits_stride, stream);
+}
+
+size_t dp_expert_sort_workspace(int64_t n, int k, int64_t experts) {
+  if (check_counts(n, k) != GRZ_OK || experts < 1 || experts > GRZ_MAX_EXPERTS) return 0;
+  const int64_t slots = n * k;
+  if (slots <= kDirectSlots) return 0;
+  return static_cast<size_t>(ceil_div(slots, tile_of(slots))) * experts * sizeof(uint32_t);
+}
+
+int dp_expert_sort(const void* ids, int id_bits, int64_t n, int k, int64_t experts,
+                   void* workspace, int32_t* offsets, int32_t* places, hipStream_t stream) {
+  int st = check_counts(n, k);
+  if (st != GRZ_OK) return st;
+  if (experts < 1) return GRZ_EINVAL;
+  if (experts > GRZ_MAX_EXPERTS) return GRZ_ERANGE;
+  if ((st = check_ids(ids, id_bits, n * k)) != GRZ_OK) return st;
+  if (offsets == nullptr) return GRZ_EINVAL;
+  if (!aligned(offsets, 4)) return GRZ_EALIGN;
+  if ((st = check_slots(places, n, k)) != GRZ_OK) return st;
+  const size_t need = dp_expert_sort_workspace(n, k, experts);
+  if (need > 0) {
+    if (workspace == nullptr) return GRZ_EINVAL;
+    if (!aligned(workspace, 4)) return GRZ_EALIGN;
+  }
+  const int64_t slots = n * k;
+  const Span in{ids, static_cast<size_t>(slots) * (id_bits / 8)}, ws{workspace, need};
+  const Span off{offsets, static_cast<size_t>(experts + 1) * 4}, pl = slot_span(places, n, k);
+  if (clash(off, {in, ws, pl}) || clash(pl, {in, ws}) || clash(ws, {in})) return GRZ_EINVAL;
+  SortArgs a;
+  a.ids = ids;
+  a.id_bits = id_bits;
+  a.slots = slots;
+  a.experts = static_cast<int>(experts);
+  a.bits = bits_of(a.experts);
+  a.tile = tile_of(slots);
+  a.tiles = static_cast<int>(slots > 0 ? ceil_div(slots, a.tile) : 1);
+  a.counts = static_cast<uint32_t*>(workspace);
+  a.offsets = offsets;
+  a.places = places;
+  const bool direct = slots <= kDirectSlots;
+  if (!direct) {
+    st = launch(expert_count_kernel, dim3(a.tiles), dim3(kSortThreads), stream, a);
+    if (st != GRZ_OK) return st;
+  }
+  return launch_lds(direct ? expert_place_kernel<true> : expert_place_kernel<false>,
+                    static_cast<size_t>(kSortWaves) * a.experts * sizeof(uint16_t), dim3(a.tiles),
+                    dim3(kSortThreads), stream, a);
+}
+
+int dp_expert_dispatch(const void* x, int x_dtype, int64_t x_stride, const int32_t* places,
+                       const float* weights, int64_t n, int k, int64_t dim, int64_t rows,
+                       void* out, int out_dtype, int64_t out_stride, hipStream_t stream) {
+  int st = check_counts(n, k);
+  if (st != GRZ_OK) return st;
+  if (dim > kCols) return GRZ_ERANGE;
+  if ((st = check_matrix(x, x_dtype, n, dim, x_stride)) != GRZ_OK) return st;
+  if ((st = check_matrix(out, out_dtype, rows, dim, out_stride)) != GRZ_OK) return st;
+  if ((st = check_slots(places, n, k)) != GRZ_OK) return st;
+  if ((st = check_slots(weights, n, k, true)) != GRZ_OK) return st;
+  if (n == 0 || dim == 0 || rows == 0) return GRZ_OK;
+  if (clash(matrix_span(out, out_dtype, rows, dim, out_stride),
+            {matrix_span(x, x_dtype, n, dim, x_stride), slot_span(places, n, k),
+             slot_span(weights, n, k)}))
+    return GRZ_EINVAL;
+#define GRZ_CALL(TI, TO)                                                                        \
+  dispatch_run<TI, TO>(x, x_stride, places, weights, n, k, dim, rows, out, out_stride, stream)
+  if (x_dtype == GRZ_BF16)
+    return out_dtype == GRZ_BF16 ? GRZ_CALL(uint16_t, uint16_t) : GRZ_CALL(uint16_t, float);
+  return out_dtype == GRZ_BF16 ? GRZ_CALL(float, uint16_t) : GRZ_CALL(float, float);
+#undef GRZ_CALL
+}
+
+int dp_expert_combine(const void* y, int y_dtype, int64_t y_stride, int64_t rows,
+                      const int32_t* places, const float* weights, int64_t n, int k, int64_t dim,
+                      int flags, void* out, int out_dtype, int64_t out_stride,
+                      hipStream_t stream) {
+  if (flags & ~GRZ_ACCUMULATE) return GRZ_EINVAL;
+  int st = check_counts(n, k);
+  if (st != GRZ_OK) return st;
+  if (dim > kCols) return GRZ_ERANGE;
+  if ((st = check_matrix(y, y_dtype, rows, dim, y_stride)) != GRZ_OK) return st;
+  if ((st = check_matrix(out, out_dtype, n, dim, out_stride)) != GRZ_OK) return st;
+  if ((st = check_slots(places, n, k)) != GRZ_OK) return st;
+  if ((st = check_slots(weights, n, k, true)) != GRZ_OK) return st;
+  if (n == 0 || dim == 0) return GRZ_OK;
+  if (clash(matrix_span(out, out_dtype, n, dim, out_stride),
+            {matrix_span(y, y_dtype, rows, dim, y_stride), slot_span(places, n, k),
+             slot_span(weights, n, k)}))
+    return GRZ_EINVAL;
+  const bool acc = flags & GRZ_ACCUMULATE;
+#define GRZ_CALL(TI, TO)                                                                         \
+  (acc ? combine_run<TI, TO, true>(y, y_stride, rows, places, weights, n, k, dim, out,           \
+                                   out_stride, stream)                                           \
+       : combine_run<TI, TO, false>(y, y_stride, rows, places, weights, n, k, dim, out,          \
+                                    out_stride, stream))
+  if (y_dtype == GRZ_BF16)
+    return out_dtype == GRZ_BF16 ? GRZ_CALL(uint16_t, uint16_t) : GRZ_CALL(uint16_t, float);
+  return out_dtype == GRZ_BF16 ? GRZ_CALL(float, uint16_t) : GRZ_CALL(float, float);
+#undef GRZ_CALL
+}
+
+int dp_expert_combine_grad(const void* dout, int dout_dtype, int64_t dout_stride, const void* y,
+                           int y_dtype, int64_t y_stride, int64_t rows, const int32_t* places,
+                           const float* weights, int64_t n, int k, int64_t dim, void* dy,
+                           int64_t dy_stride, float* dweights, hipStream_t stream) {
+  int st = check_counts(n, k);
+  if (st != GRZ_OK) return st;
+  if (dim > kCols) return GRZ_ERANGE;
+  if ((st = check_matrix(dout, dout_dtype, n, dim, dout_stride)) != GRZ_OK) return st;
+  // y is read for the weights' gradient alone.
+  st = dweights != nullptr ? check_matrix(y, y_dtype, rows, dim, y_stride)
+                           : check_matrix(nullptr, y_dtype, rows, 0, 0);
+  if (st != GRZ_OK) return st;
+  if (dy == nullptr && dweights == nullptr)
+    return n == 0 || rows == 0 || dim == 0 ? GRZ_OK : GRZ_EINVAL;
+  if (dy != nullptr && (st = check_matrix(dy, y_dtype, rows, dim, dy_stride)) != GRZ_OK)
+    return st;
+  if ((st = check_slots(places, n, k)) != GRZ_OK) return st;
+  if ((st = check_slots(weights, n, k, true)) != GRZ_OK) return st;
+  if ((st = check_slots(dweights, n, k, true)) != GRZ_OK) return st;
+  if (n == 0) return GRZ_OK;
+  const Span d = matrix_span(dout, dout_dtype, n, dim, dout_stride);
+  const Span in = dweights != nullptr ? matrix_span(y, y_dtype, rows, dim, y_stride) : Span{};
+  const Span out = matrix_span(dy, y_dtype, rows, dim, dy_stride);
+  const Span pl = slot_span(places, n, k), w = slot_span(weights, n, k);
+  const Span dw = slot_span(dweights, n, k);
+  if (clash(out, {d, pl, w, dw}) || clash(dw, {d, in, pl, w})) return GRZ_EINVAL;
+  if (!(dy == y && dy_stride == y_stride) && clash(out, {in})) return GRZ_EINVAL;
+#define GRZ_CALL(TD, TY)                                                                        \
+  combine_grad_run<TD, TY>(dout, dout_stride, y, y_stride, rows, places, weights, n, k, dim, dy, \
+                           dy_stride, dweights, stream)
+  if (dout_dtype == GRZ_BF16)
+    return y_dtype == GRZ_BF16 ? GRZ_CALL(uint16_t, uint16_t) : GRZ_CALL(uint16_t, float);
+  return y_dtype == GRZ_BF16 ? GRZ_CALL(float, uint16_t) : GRZ_CALL(float, float);
+#undef GRZ_CALL
+}
+
+}  // extern "C"

@@ -1,0 +1,481 @@
+// tensors.hip -- HIP kernels and C ABI of the gradient norm over many tensors and
+// their clipping for AMD Instinct MI355X (gfx950, CDNA4, wave64):
+//   dp_grad_sqnorm_tensors  squared norm and clip factor over a list of tensors
+//   dp_grad_clip_tensors    the list scaled by the factor, in place or elsewhere
+//
+// Gradients that sit in no arena (a rank's own experts) count in the same norm as
+// the arena's: the list's piece sums are formed as the reduce forms the arena's and
+// go through the same tree.  The list travels in the kernel arguments, kListed
+// tensors a launch: nothing is copied to the device, so a list may change from step
+// to step and a captured graph holds its own.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <new>
+
+#include <limits.h>
+#include <stdint.h>
+
+#include "grz.h"
+#include "rows.h"
+
+namespace {
+
+// Elements of all tensors of a call: their pieces' waves stay below 2^32 threads.
+constexpr int64_t kMaxElements = int64_t{1} << 37;
+constexpr int64_t kMaxPieces = int64_t{4096} * 4096 * 4096;  // of the norm's tree
+
+template <int LISTED> struct List {
+  int count;
+  uint32_t first[LISTED + 1];  // the tensor's first piece in this launch
+  uint8_t type[LISTED];
+  int64_t numel[LISTED];
+  const void* data[LISTED];
+};
+struct NormArgs {
+  static constexpr int kListed = 184;
+  List<kListed> list;
+  double* pieces;
+  bool stream;
+};
+struct ClipArgs {
+  static constexpr int kListed = 128;
+  List<kListed> list;
+  uint8_t out_type[kListed];
+  void* out[kListed];
+  const float* scale;
+  bool stream;
+};
+static_assert(sizeof(NormArgs) <= 4096 && sizeof(ClipArgs) <= 4096,
+              "a launch's arguments exceed 4 KB");
+
+// The tensor that holds a piece: the last one whose first piece is not behind it.
+template <int LISTED>
+__device__ __forceinline__ int tensor_of(const List<LISTED>& l, uint32_t piece) {
+  int lo = 0, hi = l.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (l.first[mid] <= piece) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The wave's piece in its tensor.
+struct Piece {
+  int tensor;
+  uint32_t number;  // in this launch
+  int64_t at;       // its first element
+  int64_t left;     // elements from there on
+};
+template <int LISTED>
+__device__ __forceinline__ Piece piece_of(const List<LISTED>& l, uint32_t number) {
+  Piece p;
+  p.tensor = tensor_of(l, number);
+  p.number = number;
+  p.at = static_cast<int64_t>(number - l.first[p.tensor]) * GRZ_PIECE;
+  p.left = l.numel[p.tensor] - p.at;
+  return p;
+}
+
+// 16 or 8 bytes at any element's address.
+template <bool STREAM> __device__ __forceinline__ u32x4 load16(const void* p) {
+  const u32x4e* q = static_cast<const u32x4e*>(p);
+  if constexpr (STREAM) return __builtin_nontemporal_load(q);
+  else return *q;
+}
+template <bool STREAM> __device__ __forceinline__ u32x2 load8(const void* p) {
+  const u32x2e* q = static_cast<const u32x2e*>(p);
+  if constexpr (STREAM) return __builtin_nontemporal_load(q);
+  else return *q;
+}
+template <bool STREAM> __device__ __forceinline__ void store16(void* p, u32x4 v) {
+  u32x4e* q = static_cast<u32x4e*>(p);
+  if constexpr (STREAM) __builtin_nontemporal_store(v, q);
+  else *q = v;
+}
+template <bool STREAM> __device__ __forceinline__ void store8(void* p, u32x2 v) {
+  u32x2e* q = static_cast<u32x2e*>(p);
+  if constexpr (STREAM) __builtin_nontemporal_store(v, q);
+  else *q = v;
+}
+
+// ---------------------------------------------------------------------------
+// Piece sums, one wave a piece.  Their bits are those of the reduce's piece sums:
+// thread t of 256 takes elements 1024 k + 4 t .. + 3 for k = 0 .. 3, squares added in
+// fp64 in that order, then a balanced tree over each 64 threads and (w0 + w1) + (w2 +
+// w3).  A lane stands for four of those threads: with fp32 elements for t = lane +
+// 64 w (16 accesses of 16 bytes), with bf16 for t = 2 lane and 2 lane + 1 of each half
+// (8 accesses of 16 bytes), whose first addition is then its own.
+
+template <int CTRL> __device__ __forceinline__ double add_swapped(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(b), CTRL, 0xf, 0xf,
+                                                  false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<uint32_t>(b >> 32), CTRL, 0xf,
+                                                  0xf, false);
+  return v + __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(b), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(b >> 32), lane);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// Sums over each row of 16 lanes, in all of them.
+__device__ __forceinline__ double row_sum(double v) {
+  v = add_swapped<kSwap1>(v);
+  v = add_swapped<kSwap2>(v);
+  v = add_swapped<kHalfMirror>(v);
+  return add_swapped<kMirror>(v);
+}
+
+__device__ __forceinline__ void add_square(double& s, float x) {
+  s = __fma_rn(static_cast<double>(x), static_cast<double>(x), s);
+}
+
+template <bool STREAM>
+__device__ __forceinline__ double piece_sum(const uint16_t* p, int64_t left, int lane) {
+  double s[2][2] = {};  // [half of the threads][thread of the lane's pair]
+  if (left >= GRZ_PIECE) {
+    u32x4 u[4][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        u[k][h] = load16<STREAM>(p + 1024 * k + 512 * h + 8 * lane);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          add_square(s[h][i >> 1], __uint_as_float(u[k][h][i] << 16));
+          add_square(s[h][i >> 1], __uint_as_float(u[k][h][i] & 0xffff0000u));
+        }
+  } else {
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = 1024 * k + 512 * h + 8 * lane + i;
+          if (e < left) add_square(s[h][i >> 2], widen(p[e]));
+        }
+  }
+  double w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    double v = s[h][0] + s[h][1];
+    v = add_swapped<kSwap1>(v);
+    v = add_swapped<kSwap2>(v);
+    v = add_swapped<kHalfMirror>(v);
+    v = add_swapped<kMirror>(v);
+    w[h] = (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+  }
+  return w[0] + w[1];
+}
+
+template <bool STREAM>
+__device__ __forceinline__ double piece_sum(const float* p, int64_t left, int lane) {
+  double s[4] = {};
+  if (left >= GRZ_PIECE) {
+    u32x4 u[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        u[k][w] = load16<STREAM>(p + 1024 * k + 256 * w + 4 * lane);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) add_square(s[w], __uint_as_float(u[k][w][i]));
+  } else {
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = 1024 * k + 256 * w + 4 * lane + i;
+          if (e < left) add_square(s[w], p[e]);
+        }
+  }
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const double v = row_sum(s[w]);
+    s[w] = (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+template <bool STREAM>
+__device__ __forceinline__ double piece_sum_of(const NormArgs& a, const Piece& p, int lane) {
+  const void* data = a.list.data[p.tensor];
+  return a.list.type[p.tensor] == GRZ_BF16
+             ? piece_sum<STREAM>(static_cast<const uint16_t*>(data) + p.at, p.left, lane)
+             : piece_sum<STREAM>(static_cast<const float*>(data) + p.at, p.left, lane);
+}
+
+__global__ __launch_bounds__(256) void tensors_norm_kernel(const NormArgs a) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t number =
+      blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (number >= a.list.first[a.list.count]) return;
+  const Piece p = piece_of(a.list, number);
+  const double sum = a.stream ? piece_sum_of<true>(a, p, lane) : piece_sum_of<false>(a, p, lane);
+  if (lane == 0) a.pieces[number] = sum;
+}
+
+// ---------------------------------------------------------------------------
+// Scaling, one wave a piece.
+
+template <bool STREAM, typename TI, typename TO>
+__device__ __forceinline__ void scale_piece(const TI* p, TO* q, int64_t left, float scale,
+                                            int lane) {
+  constexpr int E = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
+  constexpr int K = GRZ_PIECE / (64 * E);
+  if (left < GRZ_PIECE) {
+    for (int e = lane; e < left; e += 64) put(q + e, widen(p[e]) * scale);
+    return;
+  }
+  constexpr int IW = E * sizeof(TI) / 4, OW = E * sizeof(TO) / 4;  // words of an access
+  using In = uint32_t __attribute__((ext_vector_type(IW)));
+  using Out = uint32_t __attribute__((ext_vector_type(OW)));
+  In u[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if constexpr (IW == 4) u[k] = load16<STREAM>(p + 64 * E * k + E * lane);
+    else u[k] = load8<STREAM>(p + 64 * E * k + E * lane);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    float x[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      if constexpr (sizeof(TI) == 2)
+        x[i] = __uint_as_float(i & 1 ? u[k][i / 2] & 0xffff0000u : u[k][i / 2] << 16) * scale;
+      else
+        x[i] = __uint_as_float(u[k][i]) * scale;
+    }
+    Out o;
+    if constexpr (sizeof(TO) == 2) {
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) o[i] = bf16_bits(x[2 * i]) | bf16_bits(x[2 * i + 1]) << 16;
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] = __float_as_uint(x[i]);
+    }
+    if constexpr (OW == 4) store16<STREAM>(q + 64 * E * k + E * lane, o);
+    else store8<STREAM>(q + 64 * E * k + E * lane, o);
+  }
+}
+
+template <bool STREAM>
+__device__ __forceinline__ void scale_piece_of(const ClipArgs& a, const Piece& p, float scale,
+                                               int lane) {
+  const void* in = a.list.data[p.tensor];
+  void* out = a.out[p.tensor];
+  const uint16_t* hi = static_cast<const uint16_t*>(in) + p.at;
+  const float* fi = static_cast<const float*>(in) + p.at;
+  uint16_t* ho = static_cast<uint16_t*>(out) + p.at;
+  float* fo = static_cast<float*>(out) + p.at;
+  if (a.list.type[p.tensor] == GRZ_BF16) {
+    if (a.out_type[p.tensor] == GRZ_BF16) scale_piece<STREAM>(hi, ho, p.left, scale, lane);
+    else scale_piece<STREAM>(hi, fo, p.left, scale, lane);
+  } else {
+    if (a.out_type[p.tensor] == GRZ_BF16) scale_piece<STREAM>(fi, ho, p.left, scale, lane);
+    else scale_piece<STREAM>(fi, fo, p.left, scale, lane);
+  }
+}
+
+__global__ __launch_bounds__(256) void tensors_clip_kernel(const ClipArgs a) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t number =
+      blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t pieces = a.list.first[a.list.count];
+  if (number >= pieces) return;
+  const float scale = a.scale != nullptr ? *a.scale : 1.0f;
+  const Piece p = piece_of(a.list, pieces - 1 - number);
+  // A gradient in its place that is scaled by 1 is what it was.
+  if (scale == 1.0f && a.list.data[p.tensor] == a.out[p.tensor]) return;
+  if (a.stream) scale_piece_of<true>(a, p, scale, lane);
+  else scale_piece_of<false>(a, p, scale, lane);
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+int check_tensors(const grz_tensor* t, int64_t count, int64_t* elements, int64_t* bytes) {
+  if (count < 0 || (count > 0 && t == nullptr)) return GRZ_EINVAL;
+  *elements = *bytes = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (t[i].numel < 0 || !float_type(t[i].dtype)) return GRZ_EINVAL;
+    if (t[i].numel > kMaxElements - *elements) return GRZ_ERANGE;
+    if (t[i].numel > 0 && t[i].data == nullptr) return GRZ_EINVAL;
+    if (!aligned(t[i].data, elem_size(t[i].dtype))) return GRZ_EALIGN;
+    *elements += t[i].numel;
+    *bytes += t[i].numel * static_cast<int64_t>(elem_size(t[i].dtype));
+  }
+  return GRZ_OK;
+}
+
+int64_t pieces_of(int64_t numel) { return ceil_div(numel, GRZ_PIECE); }
+
+int64_t pieces_of(const grz_tensor* t, int64_t count) {
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) n += pieces_of(t[i].numel);
+  return n;
+}
+
+size_t bytes_of(const grz_tensor& t) { return static_cast<size_t>(t.numel) * elem_size(t.dtype); }
+
+bool clash(const void* p, size_t bytes, const grz_tensor* t, int64_t count) {
+  for (int64_t i = 0; i < count; ++i)
+    if (overlap(p, bytes, t[i].data, bytes_of(t[i]))) return true;
+  return false;
+}
+
+// Whether a tensor that is written lies over another one, read or written; only a
+// gradient and its own output may be the same memory.
+struct Range {
+  uintptr_t from, to;
+  bool out;
+};
+
+int check_apart(const grz_tensor* in, const grz_tensor* out, int64_t count) {
+  Range few[64];
+  Range* r = few;
+  if (2 * count > 64) {
+    r = new (std::nothrow) Range[static_cast<size_t>(2 * count)];
+    if (r == nullptr) return GRZ_ERANGE;
+  }
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (in[i].numel == 0) continue;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(in[i].data);
+    const uintptr_t b = reinterpret_cast<uintptr_t>(out[i].data);
+    r[n++] = {b, b + bytes_of(out[i]), true};
+    if (a != b || in[i].dtype != out[i].dtype) r[n++] = {a, a + bytes_of(in[i]), false};
+  }
+  auto before = [](const Range& x, const Range& y) { return x.from < y.from; };
+  if (!std::is_sorted(r, r + n, before)) std::sort(r, r + n, before);
+  uintptr_t any = 0, written = 0;  // ends of the ranges so far
+  int st = GRZ_OK;
+  for (int64_t i = 0; i < n && st == GRZ_OK; ++i) {
+    if (r[i].from < (r[i].out ? any : written)) st = GRZ_EINVAL;
+    any = std::max(any, r[i].to);
+    if (r[i].out) written = std::max(written, r[i].to);
+  }
+  if (r != few) delete[] r;
+  return st;
+}
+
+// Bytes from which the tensors are streamed past the caches: what is much larger than
+// the 256 MB behind the L2s is not there any more when it is read again.
+constexpr int64_t kStreamBytes = int64_t{192} << 20;
+
+// Appends tensors from `i` on to an empty list until it is full; returns the next one.
+template <int LISTED, typename F>
+int64_t fill(List<LISTED>& l, const grz_tensor* t, int64_t i, int64_t count, F also) {
+  l.count = 0;
+  l.first[0] = 0;
+  for (; i < count && l.count < LISTED; ++i) {
+    if (t[i].numel == 0) continue;
+    l.data[l.count] = t[i].data;
+    l.numel[l.count] = t[i].numel;
+    l.type[l.count] = static_cast<uint8_t>(t[i].dtype);
+    also(l.count, i);
+    l.first[l.count + 1] = l.first[l.count] + static_cast<uint32_t>(pieces_of(t[i].numel));
+    ++l.count;
+  }
+  return i;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// C ABI
+
+extern "C" {
+
+int64_t dp_tensor_pieces(const grz_tensor* tensors, int64_t count) {
+  int64_t elements, bytes;
+  const int st = check_tensors(tensors, count, &elements, &bytes);
+  return st != GRZ_OK ? -st : pieces_of(tensors, count);
+}
+
+size_t dp_grad_sqnorm_tensors_workspace(const grz_tensor* tensors, int64_t count, int64_t lead) {
+  const int64_t n = dp_tensor_pieces(tensors, count);
+  if (n < 0 || lead < 0 || lead > kMaxPieces - n) return 0;
+  return static_cast<size_t>(n + lead) * sizeof(double) + dp_grad_sqnorm_workspace(n + lead);
+}
+
+int dp_grad_sqnorm_tensors(const grz_tensor* tensors, int64_t count, double max_norm,
+                           int64_t lead, void* workspace, double* sqnorm_out,
+                           float* clip_scale_out, hipStream_t stream) {
+  int64_t elements, bytes;
+  int st = check_tensors(tensors, count, &elements, &bytes);
+  if (st != GRZ_OK) return st;
+  const int64_t n = pieces_of(tensors, count);
+  if (lead < 0) return GRZ_EINVAL;
+  if (lead > kMaxPieces - n) return GRZ_ERANGE;
+  const size_t need = dp_grad_sqnorm_tensors_workspace(tensors, count, lead);
+  if (need > 0 && workspace == nullptr) return GRZ_EINVAL;
+  if (sqnorm_out == nullptr && clip_scale_out == nullptr) return GRZ_EINVAL;
+  if (!aligned(workspace, 8) || !aligned(sqnorm_out, 8) || !aligned(clip_scale_out, 4))
+    return GRZ_EALIGN;
+  const size_t sq = sqnorm_out != nullptr ? 8 : 0, sc = clip_scale_out != nullptr ? 4 : 0;
+  if (clash(workspace, need, tensors, count) || clash(sqnorm_out, sq, tensors, count) ||
+      clash(clip_scale_out, sc, tensors, count) || overlap(workspace, need, sqnorm_out, sq) ||
+      overlap(workspace, need, clip_scale_out, sc) || overlap(sqnorm_out, sq, clip_scale_out, sc))
+    return GRZ_EINVAL;
+  double* const pieces = static_cast<double*>(workspace);
+  NormArgs a;
+  a.pieces = pieces + lead;
+  a.stream = bytes >= kStreamBytes;
+  for (int64_t i = 0; i < count;) {
+    i = fill(a.list, tensors, i, count, [](int, int64_t) {});
+    const uint32_t k = a.list.first[a.list.count];
+    if (k == 0) continue;
+    st = launch(tensors_norm_kernel, dim3(static_cast<unsigned>(ceil_div(k, 4))), dim3(256),
+                stream, a);
+    if (st != GRZ_OK) return st;
+    a.pieces += k;
+  }
+  return dp_grad_sqnorm(pieces, n + lead, max_norm, pieces + n + lead, sqnorm_out,
+                        clip_scale_out, stream);
+}
+
+int dp_grad_clip_tensors(const grz_tensor* grads, int64_t count, const float* clip_scale,
+                         const grz_tensor* out, hipStream_t stream) {
+  int64_t elements, bytes, out_bytes;
+  int st = check_tensors(grads, count, &elements, &bytes);
+  if (st != GRZ_OK) return st;
+  if (!aligned(clip_scale, 4)) return GRZ_EALIGN;
+  if (out == nullptr) out = grads;
+  if ((st = check_tensors(out, count, &elements, &out_bytes)) != GRZ_OK) return st;
+  for (int64_t i = 0; i < count; ++i)
+    if (out[i].numel != grads[i].numel) return GRZ_EINVAL;
+  if (clip_scale != nullptr && clash(clip_scale, 4, out, count)) return GRZ_EINVAL;
+  if ((st = check_apart(grads, out, count)) != GRZ_OK) return st;
+  ClipArgs a;
+  a.scale = clip_scale;
+  a.stream = bytes >= kStreamBytes;
+  for (int64_t i = 0; i < count;) {
+    i = fill(a.list, grads, i, count, [&](int to, int64_t from) {
+      a.out[to] = out[from].data;
+      a.out_type[to] = static_cast<uint8_t>(out[from].dtype);
+    });
+    const uint32_t k = a.list.first[a.list.count];
+    if (k == 0) continue;
+    st = launch(tensors_clip_kernel, dim3(static_cast<unsigned>(ceil_div(k, 4))), dim3(256),
+                stream, a);
+    if (st != GRZ_OK) return st;
+  }
+  return GRZ_OK;
+}
+
+}  // extern "C"

@@ -24,6 +24,21 @@
  *   dp_distill_loss          loss against a teacher's top logits
  *   dp_distill_grad          its gradient
  *
+ * the operators of a mixture of experts between them:
+ *
+ *   dp_expert_route          a token's experts and their weights
+ *   dp_expert_route_grad     the gradient of the weights, to the router's logits
+ *   dp_expert_sort           the tokens' slots sorted by expert
+ *   dp_expert_dispatch       the tokens' rows in that order
+ *   dp_expert_combine        rows back to their tokens, summed with the weights
+ *   dp_expert_combine_grad   gradient of that sum
+ *
+ * and the norm and the clip for gradients that are tensors of their own, beside
+ * the arena (a rank's experts) or in its place:
+ *
+ *   dp_grad_sqnorm_tensors   squared norm and clip factor over many tensors
+ *   dp_grad_clip_tensors     the tensors scaled by the factor
+ *
  * Sources: "Lab 09 -- Parallelism, simulated" s.1 "Ring all-reduce" (the
  * N = 3 schedule table; "Tips": in reduce-scatter step t rank r sends chunk
  * (r - t) mod N and ends owning chunk (r + 1) mod N) and s.2 (sum, then
@@ -104,7 +119,8 @@ enum { GRZ_F32 = 0, GRZ_BF16 = 1, GRZ_F64 = 2 };
  * GRZ_SUM; zero1_adamw_gather takes GRZ_UNEVEN, GRZ_ARGS_DEVICE and
  * GRZ_MEAN_BF16; the
  * all-gathers take GRZ_UNEVEN; zero1_fused_step GRZ_UNEVEN, GRZ_IN_COMPACT,
- * GRZ_ARGS_DEVICE and GRZ_COOPERATIVE; dp_embed_grad GRZ_ACCUMULATE.  Their
+ * GRZ_ARGS_DEVICE and GRZ_COOPERATIVE; dp_embed_grad and dp_expert_combine
+ * GRZ_ACCUMULATE; dp_expert_route and its gradient GRZ_NORMALIZE.  Their
  * meaning is in each entry point's comment. */
 enum {
   GRZ_SUM = 1,        /* keep the sum: skip the division by N            */
@@ -118,12 +134,16 @@ enum {
                            values of each piece side by side               */
   GRZ_MEAN_BF16 = 256,  /* the mean (gradient shard) is held in bf16         */
   GRZ_COOPERATIVE = 512, /* zero1_fused_step: a cooperative launch           */
-  GRZ_ACCUMULATE = 1024 /* dp_embed_grad: add to what the table gradient holds */
+  GRZ_ACCUMULATE = 1024, /* dp_embed_grad, dp_expert_combine: add to what the
+                            output holds                                    */
+  GRZ_NORMALIZE = 2048  /* dp_expert_route: the listed weights sum to 1       */
 };
 
 #define GRZ_MAX_RANKS 16    /* N and the number of replicas per call       */
 #define GRZ_PIECE 4096      /* elements per norm piece                      */
 #define GRZ_MAX_TOP 128     /* longest top list of a row                    */
+#define GRZ_MAX_EXPERTS 1024 /* experts of a mixture                         */
+#define GRZ_MAX_SLOTS 32    /* experts a token goes to                      */
 
 typedef struct {
   int64_t offset; /* first element of the bucket in the arena */
@@ -141,6 +161,14 @@ typedef struct {
   float bias_corr1;
   float bias_corr2;
 } grz_adamw_args;
+
+/* A tensor of a list: `numel` consecutive elements (GRZ_F32 or GRZ_BF16) in
+ * device memory, at any element's address. */
+typedef struct {
+  void* data;
+  int64_t numel;
+  int dtype;
+} grz_tensor;
 
 /* Version of the ABI (major * 100 + minor). */
 int grz_version(void);
@@ -702,6 +730,185 @@ int dp_distill_grad(const void* logits, int dtype, int64_t n, int64_t vocab, int
                     int teacher_dtype, int k, float temperature, const float* weights,
                     float grad_scale, float* loss, void* dlogits, int64_t dlogits_stride,
                     hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Mixture-of-experts operators: the way of n tokens to k experts each and back.
+ *
+ *   ids, weights     = dp_expert_route(router logits)
+ *   offsets, places  = dp_expert_sort(ids)
+ *   rows             = dp_expert_dispatch(x, places)
+ *   y[r]             = expert e's output for rows[r], offsets[e] <= r < offsets[e + 1]
+ *   out              = dp_expert_combine(y, places, weights)
+ * and the gradients' way:
+ *   dy, dweights     = dp_expert_combine_grad(dout, y, places, weights)
+ *   drows            = the experts' gradients for dy
+ *   dx               = dp_expert_combine(drows, places, no weights)
+ *   dlogits          = dp_expert_route_grad(dweights)
+ * (A dispatch with weights: dx = dp_expert_combine(drows, places, weights), and
+ * dweights = dp_expert_combine_grad(dout = x, y = drows) without dy.)
+ *
+ * Shared conventions: row matrices, sizes, arithmetic and errors as for the
+ * operators addressed by token ids (rows at any element's address are about as
+ * fast as those on 16-byte borders), and
+ *
+ *  - Slots.  A token has k of them (1..GRZ_MAX_SLOTS), slot j of token i at index
+ *    i * k + j of the contiguous n x k arrays.  n * k is at most 2^28, columns at
+ *    most 2^22 - 64 (GRZ_ERANGE).
+ *  - An id outside [0, experts) names no expert, a place outside [0, rows) no row:
+ *    the slot adds nothing, is stored nowhere, and what its weight and dweight
+ *    entries hold is not read.
+ *  - Places that name rows twice are an error of the caller: such a row then holds
+ *    one of its tokens' rows.  Nothing else is affected.
+ *  - Rows that no place names are left as they were.
+ */
+
+/*
+ * The k experts with the largest logits of each token, larger first, equal ones by
+ * lower id (NaN counts as largest), and their weights under p = softmax(logits[i]):
+ * p itself, or with GRZ_NORMALIZE p divided by the k weights' sum (the softmax
+ * over the listed logits).
+ *
+ * logits   device, n x experts (1..GRZ_MAX_EXPERTS).
+ * k        1..min(GRZ_MAX_SLOTS, experts).
+ * ids      device int32[n * k]; weights  device fp32[n * k].
+ * A logit of -inf closes an expert to the token: it is never listed, and where
+ * fewer than k are open the last slots have id -1 and weight 0 (all of them in a
+ * row with nothing open, a padded position).  A row that holds a NaN or +inf has
+ * no softmax: its weights are NaN (its ids are still in order).
+ * Errors: GRZ_EINVAL for k > experts; GRZ_ERANGE beyond GRZ_MAX_EXPERTS.
+ */
+int dp_expert_route(const void* logits, int dtype, int64_t n, int64_t experts, int64_t stride,
+                    int k, int flags, int32_t* ids, float* weights, hipStream_t stream);
+
+/*
+ * Gradient of dp_expert_route's weights with respect to the logits, the choice of
+ * the experts being fixed.  With w_j the weight of the expert e_j in slot j and g_j =
+ * dweights[i][j]:
+ *
+ *   dlogits[i][e] = sum over e_j = e of g_j w_j - p_e sum_j g_j w_j
+ *   with GRZ_NORMALIZE:  sum over e_j = e of w_j (g_j - sum_l g_l w_l)
+ *
+ * ids       device int32[n * k], dp_expert_route's or any others (an expert listed
+ *           twice has its slots' sum).  A listed expert that is closed has weight 0.
+ * dweights  device fp32[n * k].  A row whose slots name no expert, or only with
+ *           dweights of 0, gets zeros whatever its logits hold.
+ * dlogits   device, n x experts of the logits' type; may be the logits themselves
+ *           (same pointer and stride).
+ */
+int dp_expert_route_grad(const void* logits, int dtype, int64_t n, int64_t experts,
+                         int64_t stride, int k, int flags, const int32_t* ids,
+                         const float* dweights, void* dlogits, int64_t dlogits_stride,
+                         hipStream_t stream);
+
+/* Bytes of workspace dp_expert_sort needs (0 for few slots or sizes it refuses). */
+size_t dp_expert_sort_workspace(int64_t n, int k, int64_t experts);
+
+/*
+ * Places of the slots sorted by expert, stable (an expert's rows in the order of
+ * its tokens).
+ *
+ * ids        device, n * k ids (id_bits 32 or 64), contiguous.
+ * experts    1..GRZ_MAX_EXPERTS.
+ * workspace  device, dp_expert_sort_workspace bytes, 4-byte aligned; needs no
+ *            initial value.  Calls that may run at the same time need one each.
+ * offsets    device int32[experts + 1]: expert e's rows are offsets[e] ..
+ *            offsets[e + 1] - 1; offsets[experts] is the number of rows.
+ * places     device int32[n * k]: the slot's row, -1 where the id names no expert.
+ * n = 0 still writes the offsets.
+ */
+int dp_expert_sort(const void* ids, int id_bits, int64_t n, int k, int64_t experts,
+                   void* workspace, int32_t* offsets, int32_t* places, hipStream_t stream);
+
+/*
+ * out[places[i][j]] = weights[i][j] x[i] (x[i] itself without weights).
+ *
+ * x  device, n x dim; places  device int32[n * k]; weights  device fp32[n * k] or
+ * NULL; out  device, rows x dim; any of the two types each.
+ */
+int dp_expert_dispatch(const void* x, int x_dtype, int64_t x_stride, const int32_t* places,
+                       const float* weights, int64_t n, int k, int64_t dim, int64_t rows,
+                       void* out, int out_dtype, int64_t out_stride, hipStream_t stream);
+
+/*
+ * out[i] = sum over j of weights[i][j] y[places[i][j]] (of the rows themselves
+ * without weights), in the slots' order; with GRZ_ACCUMULATE onto what out[i]
+ * holds, rounded once.  A token without places gets zeros (or keeps its row).
+ *
+ * y  device, rows x dim; out  device, n x dim; any of the two types each; places,
+ * weights  as for dp_expert_dispatch.
+ */
+int dp_expert_combine(const void* y, int y_dtype, int64_t y_stride, int64_t rows,
+                      const int32_t* places, const float* weights, int64_t n, int k, int64_t dim,
+                      int flags, void* out, int out_dtype, int64_t out_stride,
+                      hipStream_t stream);
+
+/*
+ * Gradient of dp_expert_combine:
+ *   dy[places[i][j]] = weights[i][j] dout[i]         (1 without weights)
+ *   dweights[i][j]   = sum over the columns of dout[i] y[places[i][j]]
+ *
+ * dout      device, n x dim of either type.
+ * y         device, rows x dim (not read, and may be NULL, without dweights).
+ * dy        device, rows x dim of y's type, or NULL; may be y itself (same pointer
+ *           and stride).
+ * dweights  device fp32[n * k] or NULL (not both): 0 for a slot without a row.
+ */
+int dp_expert_combine_grad(const void* dout, int dout_dtype, int64_t dout_stride, const void* y,
+                           int y_dtype, int64_t y_stride, int64_t rows, const int32_t* places,
+                           const float* weights, int64_t n, int k, int64_t dim, void* dy,
+                           int64_t dy_stride, float* dweights, hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Gradients that are tensors of their own ("Distributed training",
+ * clip_grads_device(max_norm), for a model whose gradients are not, or not all, in
+ * the flat arena: an expert-parallel rank's experts are averaged over no rank).
+ *
+ * Lists are host arrays of grz_tensor, read during the call only; the tensors may
+ * be of both types, of any length (0 too) and at any element's address.  2^37
+ * elements in all at most (GRZ_ERANGE).
+ */
+
+/* Norm pieces of the list: GRZ_PIECE consecutive elements of one tensor each, the
+ * last of a tensor possibly shorter, numbered tensor by tensor; or a negative
+ * GRZ_E* code. */
+int64_t dp_tensor_pieces(const grz_tensor* tensors, int64_t count);
+
+/* Bytes of workspace dp_grad_sqnorm_tensors needs (0 also for what it refuses). */
+size_t dp_grad_sqnorm_tensors_workspace(const grz_tensor* tensors, int64_t count, int64_t lead);
+
+/*
+ * Global squared norm and clip factor over `lead` pieces whose sums are there
+ * already (the arena's, from dp_reduce_scatter_mean; a peer's experts') and all
+ * elements of the list: the list's piece sums, formed as the reduce forms the
+ * arena's, then dp_grad_sqnorm over all of them.  One fp32 tensor and lead 0 give
+ * the bits of dp_grad_sqnorm_of.
+ *
+ * workspace  device, dp_grad_sqnorm_tensors_workspace bytes, 8-byte aligned.  Its
+ *            first `lead` doubles are the sums that are there; on return the
+ *            list's dp_tensor_pieces follow them.  Calls that may run at the same
+ *            time need one each.
+ * max_norm, sqnorm_out, clip_scale_out  as for dp_grad_sqnorm (either output may be
+ *            NULL, not both).  A tensor listed twice counts twice.
+ */
+int dp_grad_sqnorm_tensors(const grz_tensor* tensors, int64_t count, double max_norm,
+                           int64_t lead, void* workspace, double* sqnorm_out,
+                           float* clip_scale_out, hipStream_t stream);
+
+/*
+ * out[t][e] = clip_scale grads[t][e]: one fp32 product, rounded once to the output's
+ * type.
+ *
+ * clip_scale  device fp32 scalar (dp_grad_sqnorm's output) or NULL for 1.
+ * out         host list of the same lengths (types may differ: into a flat arena,
+ *             say), or NULL to scale the gradients in place.  In place, a factor
+ *             of 1 reads and writes nothing.
+ * Errors: GRZ_EINVAL also where an output lies over another tensor of either
+ * list than its own gradient, or over that one in part.
+ */
+int dp_grad_clip_tensors(const grz_tensor* grads, int64_t count, const float* clip_scale,
+                         const grz_tensor* out, hipStream_t stream);
 
 #ifdef __cplusplus
 }
