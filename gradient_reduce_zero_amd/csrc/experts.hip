@@ -14,6 +14,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include <limits.h>
 #include <stdint.h>
 
@@ -24,39 +26,42 @@ namespace {
 
 constexpr int64_t kSlots = int64_t{1} << 28;      // n * k of one call
 constexpr int64_t kCols = int64_t{65535} * 64;    // columns: 2^16 column blocks of a launch
-constexpr int64_t kTokenBatch = int64_t{1} << 21;  // tokens of one launch
+constexpr int64_t kTokenBatch = int64_t{1} << 20;  // tokens of one launch
+constexpr int64_t kUnitBatch = int64_t{1} << 23;   // their runs of columns, a wave each
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // ---------------------------------------------------------------------------
 // Vectors of a row that begin anywhere: gfx950 reads and writes 8 and 16 bytes at
 // any element's address, so rows need no alignment of their own.
 
-template <typename T, int N>
-__device__ __forceinline__ void load_cols(const T* p, float (&x)[N]) {
-  if constexpr (sizeof(T) == 2) {
-    if constexpr (N == 8) {
-      const u32x4e u = *reinterpret_cast<const u32x4e*>(p);
+// N consecutive elements as they lie in memory (8 or 16 bytes), widened one by one
+// where they are used: many loads wait in few registers.
+template <typename T, int N> struct Cols {
+  static constexpr int kWords = N * sizeof(T) / 4;
+  static_assert(kWords == 2 || kWords == 4, "accesses of 8 or 16 bytes");
+  uint32_t w[kWords];
+  template <bool STREAM = false> __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 4) {
+      const u32x4e* q = reinterpret_cast<const u32x4e*>(p);
+      u32x4 u;
+      if constexpr (STREAM) u = __builtin_nontemporal_load(q);
+      else u = *q;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-      }
+      for (int i = 0; i < 4; ++i) w[i] = u[i];
     } else {
-      static_assert(N == 4, "bf16 vectors hold 4 or 8 elements");
-      const u32x2e u = *reinterpret_cast<const u32x2e*>(p);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-      }
+      const u32x2e* q = reinterpret_cast<const u32x2e*>(p);
+      u32x2 u;
+      if constexpr (STREAM) u = __builtin_nontemporal_load(q);
+      else u = *q;
+      w[0] = u[0];
+      w[1] = u[1];
     }
-  } else {
-    static_assert(N == 4, "fp32 vectors hold 4 elements");
-    const u32x4e u = *reinterpret_cast<const u32x4e*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(u[i]);
   }
-}
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
 
 template <typename T, int N>
 __device__ __forceinline__ void store_cols(T* p, const float (&x)[N]) {
@@ -83,6 +88,18 @@ template <typename A, typename B> constexpr int cols_of() {
 
 __device__ __forceinline__ int wave_index() {
   return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
+// A wave's token and run of columns: the runs of a token's row are neighbours, so
+// that a row is read or written at one time.
+struct Unit {
+  int64_t token;
+  int part;
+};
+__device__ __forceinline__ Unit unit_of(int64_t row0, int parts) {
+  const uint32_t unit = blockIdx.x * 4 + wave_index();
+  const uint32_t token = unit / static_cast<uint32_t>(parts);
+  return {row0 + token, static_cast<int>(unit - token * parts)};
 }
 
 // ---------------------------------------------------------------------------
@@ -161,8 +178,8 @@ __device__ __forceinline__ void load_logits(const T* row, int experts, int g, bo
     if constexpr (V >= 4) {
 #pragma unroll
       for (int h = 0; h < V / E; ++h) {
-        float y[E];
-        load_cols<T, E>(row + c + h * E, y);
+        Cols<T, E> y;
+        y.load(row + c + h * E);
 #pragma unroll
         for (int i = 0; i < E; ++i) x[h * E + i] = y[i];
       }
@@ -335,8 +352,8 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int64_t kDirectSlots = 16384;
-constexpr int64_t kMaxTiles = 256;
+constexpr int64_t kDirectSlots = 8192;
+constexpr int64_t kMaxTiles = 256, kTileCounts = 131072;
 
 struct SortArgs {
   const void* ids;
@@ -462,38 +479,32 @@ __global__ __launch_bounds__(kSortThreads) void expert_place_kernel(SortArgs a) 
 // by one by the waves of the last run.
 
 // out[places[i][j]] = (weights[i][j]) x[i]: the row is read once and stored k times.
-template <typename TI, typename TO, int U>
+template <typename TI, typename TO>
 __global__ __launch_bounds__(256) void dispatch_kernel(
     const TI* __restrict__ x, int64_t xstride, const int32_t* __restrict__ places,
-    const float* __restrict__ weights, int64_t row0, int64_t n, int k, int64_t dim, int64_t rows,
-    TO* __restrict__ out, int64_t ostride) {
+    const float* __restrict__ weights, int64_t row0, int64_t n, int k, int64_t dim, int parts,
+    int64_t rows, TO* __restrict__ out, int64_t ostride) {
   constexpr int VEC = cols_of<TI, TO>();
   const int lane = threadIdx.x & 63;
-  const int64_t token = row0 + static_cast<int64_t>(blockIdx.x) * 4 + wave_index();
+  const auto [token, run] = unit_of(row0, parts);
   if (token >= n) return;
   const TI* src = x + token * xstride;
   const int64_t whole = dim - dim % VEC;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (64 * VEC * U) + lane * VEC;
-  float v[U][VEC], last = 0.0f;
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t c = c0 + u * 64 * VEC;
-    if (c < whole) load_cols<TI, VEC>(src + c, v[u]);
-  }
-  const bool tail = blockIdx.y == gridDim.y - 1 && lane < dim - whole;
+  const int64_t c = static_cast<int64_t>(run) * (64 * VEC) + lane * VEC;
+  const bool in = c < whole, tail = run == parts - 1 && lane < dim - whole;
+  Cols<TI, VEC> v = {};
+  float last = 0.0f;
+  if (in) v.load(src + c);
   if (tail) last = widen(src[whole + lane]);
   for (int j = 0; j < k; ++j) {
     const int64_t p = places[token * k + j];
     if (p < 0 || p >= rows) continue;
     const float w = weights != nullptr ? weights[token * k + j] : 1.0f;
     TO* dst = out + p * ostride;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = c0 + u * 64 * VEC;
-      if (c >= whole) continue;
+    if (in) {
       float y[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) y[i] = v[u][i] * w;
+      for (int i = 0; i < VEC; ++i) y[i] = v[i] * w;
       store_cols<TO, VEC>(dst + c, y);
     }
     if (tail) put(dst + whole + lane, last * w);
@@ -502,30 +513,36 @@ __global__ __launch_bounds__(256) void dispatch_kernel(
 
 // out[i] = sum over j of (weights[i][j]) y[places[i][j]], added to out[i] with ACC:
 // KB rows' vectors on their way at once, summed in the slots' order.
-template <typename TI, typename TO, int U, int KB, bool ACC>
+template <typename TI, typename TO, int U, int KB, bool ACC, bool STREAM>
 __global__ __launch_bounds__(256) void combine_kernel(
     const TI* __restrict__ y, int64_t ystride, int64_t rows, const int32_t* __restrict__ places,
-    const float* __restrict__ weights, int64_t row0, int64_t n, int k, int64_t dim,
+    const float* __restrict__ weights, int64_t row0, int64_t n, int k, int64_t dim, int parts,
     TO* __restrict__ out, int64_t ostride) {
   constexpr int VEC = cols_of<TI, TO>();
   const int lane = threadIdx.x & 63;
-  const int64_t token = row0 + static_cast<int64_t>(blockIdx.x) * 4 + wave_index();
+  const auto [token, run] = unit_of(row0, parts);
   if (token >= n) return;
   TO* dst = out + token * ostride;
   const int64_t whole = dim - dim % VEC;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (64 * VEC * U) + lane * VEC;
-  const bool tail = blockIdx.y == gridDim.y - 1 && lane < dim - whole;
+  const int64_t c0 = static_cast<int64_t>(run) * (64 * VEC * U) + lane * VEC;
+  const bool tail = run == parts - 1 && lane < dim - whole;
   float acc[U][VEC], last = 0.0f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[u][i] = 0.0f;
     const int64_t c = c0 + u * 64 * VEC;
-    if (ACC && c < whole) load_cols<TO, VEC>(dst + c, acc[u]);
+    if (ACC && c < whole) {
+      Cols<TO, VEC> old;
+      old.load(dst + c);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[u][i] = old[i];
+    }
   }
   if (ACC && tail) last = widen(dst[whole + lane]);
   for (int j0 = 0; j0 < k; j0 += KB) {
-    float v[KB][U][VEC], w[KB];
+    Cols<TI, VEC> v[KB][U] = {};
+    float w[KB];
     int64_t p[KB];
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
@@ -534,10 +551,8 @@ __global__ __launch_bounds__(256) void combine_kernel(
       w[b] = weights != nullptr && p[b] >= 0 ? weights[token * k + j0 + b] : 1.0f;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[b][u][i] = 0.0f;
         const int64_t c = c0 + u * 64 * VEC;
-        if (p[b] >= 0 && c < whole) load_cols<TI, VEC>(y + p[b] * ystride + c, v[b][u]);
+        if (p[b] >= 0 && c < whole) v[b][u].template load<STREAM>(y + p[b] * ystride + c);
       }
     }
 #pragma unroll
@@ -559,95 +574,65 @@ __global__ __launch_bounds__(256) void combine_kernel(
 }
 
 // dy[places[i][j]] = weights[i][j] dout[i] and dweights[i][j] = <dout[i],
-// y[places[i][j]]>: W waves to a token, each with every W-th run of columns; the
-// rows' products are summed over the lanes, then over the waves.  dy may be y: a
-// lane stores where it has read.
-template <typename TD, typename TY, int U, int KB, int W>
-__global__ __launch_bounds__(256) void combine_grad_kernel(
+// y[places[i][j]]>: a wave to a slot, so that it streams one row of y and one of dy;
+// the token's other slots are its neighbours and find dout[i] in the caches.  U
+// vectors of each row on their way at once.  dy may be y: a lane stores where it has
+// read.
+constexpr int kGradWaves = 8;  // of a workgroup
+
+template <typename TD, typename TY, int U, bool STREAM>
+__global__ __launch_bounds__(kGradWaves * 64) void combine_grad_kernel(
     const TD* __restrict__ dout, int64_t dstride, const TY* y, int64_t ystride, int64_t rows,
     const int32_t* __restrict__ places, const float* __restrict__ weights, int64_t row0,
     int64_t n, int k, int64_t dim, TY* dy, int64_t dystride, float* __restrict__ dweights) {
   constexpr int VEC = cols_of<TD, TY>();
-  __shared__ float part[4][KB];
-  const int lane = threadIdx.x & 63, wave = wave_index();
-  const int64_t token = row0 + static_cast<int64_t>(blockIdx.x) * (4 / W) + wave / W;
-  if (token >= n) return;  // W = 4: the whole workgroup
+  const int lane = threadIdx.x & 63;
+  const uint32_t unit = blockIdx.x * kGradWaves + wave_index();
+  const int64_t token = row0 + unit / static_cast<uint32_t>(k);
+  if (token >= n) return;
+  const int64_t slot = row0 * k + unit;
+  const int64_t p = places[slot];
+  if (p < 0 || p >= rows) {
+    if (dweights != nullptr && lane == 0) dweights[slot] = 0.0f;
+    return;
+  }
+  const float w = weights != nullptr ? weights[slot] : 1.0f;
   const TD* src = dout + token * dstride;
+  const TY* in = y + p * ystride;
+  TY* dst = dy + p * dystride;
   const int64_t whole = dim - dim % VEC;
-  const bool tail = wave % W == 0 && lane < dim - whole;
-  for (int j0 = 0; j0 < k; j0 += KB) {
-    float w[KB], dot[KB];
-    int64_t p[KB];
+  float dot = 0.0f;
+  for (int64_t c0 = lane * VEC; c0 < whole; c0 += 64 * VEC * U) {
+    Cols<TD, VEC> d[U] = {};
+    Cols<TY, VEC> v[U] = {};
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      p[b] = j0 + b < k ? places[token * k + j0 + b] : -1;
-      if (p[b] >= rows) p[b] = -1;
-      w[b] = weights != nullptr && p[b] >= 0 ? weights[token * k + j0 + b] : 1.0f;
-      dot[b] = 0.0f;
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = c0 + u * 64 * VEC;
+      if (c >= whole) continue;
+      d[u].load(src + c);
+      if (dweights != nullptr) v[u].template load<STREAM>(in + c);
     }
-    for (int64_t c0 = (wave % W) * (64 * VEC * U) + lane * VEC; c0 < whole;
-         c0 += W * 64 * VEC * U) {
-      float d[U][VEC], v[KB][U][VEC];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t c = c0 + u * 64 * VEC;
-        if (c < whole) load_cols<TD, VEC>(src + c, d[u]);
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = c0 + u * 64 * VEC;
+      if (c >= whole) continue;
 #pragma unroll
-        for (int b = 0; b < KB; ++b)
-          if (p[b] >= 0 && dweights != nullptr && c < whole)
-            load_cols<TY, VEC>(y + p[b] * ystride + c, v[b][u]);
-      }
+      for (int i = 0; i < VEC; ++i) dot = fmaf(d[u][i], v[u][i], dot);
+      if (dy == nullptr) continue;
+      float o[VEC];
 #pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        if (p[b] < 0) continue;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t c = c0 + u * 64 * VEC;
-          if (c >= whole) continue;
-          if (dweights != nullptr) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) dot[b] = fmaf(d[u][i], v[b][u][i], dot[b]);
-          }
-          if (dy != nullptr) {
-            float o[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = d[u][i] * w[b];
-            store_cols<TY, VEC>(dy + p[b] * dystride + c, o);
-          }
-        }
-      }
-    }
-    if (tail) {
-      const float d = widen(src[whole + lane]);
-#pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        if (p[b] < 0) continue;
-        if (dweights != nullptr)
-          dot[b] = fmaf(d, widen(y[p[b] * ystride + whole + lane]), dot[b]);
-        if (dy != nullptr) put(dy + p[b] * dystride + whole + lane, d * w[b]);
-      }
-    }
-    if (dweights == nullptr) continue;
-#pragma unroll
-    for (int b = 0; b < KB; ++b) dot[b] = wave_sum(dot[b]);
-    if constexpr (W > 1) {
-      if (lane == 0) {
-#pragma unroll
-        for (int b = 0; b < KB; ++b) part[wave][b] = dot[b];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int b = 0; b < KB; ++b)
-        dot[b] = (part[0][b] + part[1][b]) + (part[2][b] + part[3][b]);
-      __syncthreads();
-    }
-    if (wave % W == 0) {
-#pragma unroll
-      for (int b = 0; b < KB; ++b)
-        if (lane == b && j0 + b < k)
-          dweights[token * k + j0 + b] = p[b] < 0 ? 0.0f : dot[b];
+      for (int i = 0; i < VEC; ++i) o[i] = d[u][i] * w;
+      store_cols<TY, VEC>(dst + c, o);
     }
   }
+  if (lane < dim - whole) {
+    const float d = widen(src[whole + lane]);
+    if (dweights != nullptr) dot = fmaf(d, widen(in[whole + lane]), dot);
+    if (dy != nullptr) put(dst + whole + lane, d * w);
+  }
+  if (dweights == nullptr) return;
+  dot = wave_sum(dot);
+  if (lane == 0) dweights[slot] = dot;
 }
 
 // ---------------------------------------------------------------------------
@@ -738,32 +723,37 @@ int check_route(const void* logits, int dtype, int64_t n, int64_t experts, int64
   return st != GRZ_OK ? st : check_matrix(logits, dtype, n, experts, stride);
 }
 
-int64_t tile_of(int64_t slots) {
-  return slots <= kDirectSlots
-             ? kSortThreads
-             : ceil_div(slots, kMaxTiles * kSortThreads) * kSortThreads;
+// Every workgroup reads all tiles' counts, so many experts get fewer, longer tiles.
+int64_t tile_of(int64_t slots, int64_t experts) {
+  if (slots <= kDirectSlots) return kSortThreads;
+  const int64_t tiles = std::min(kMaxTiles, kTileCounts / experts);
+  return ceil_div(slots, tiles * kSortThreads) * kSortThreads;
 }
 int bits_of(int v) {
   int b = 1;
   while (v >> b) ++b;
   return b;
 }
+// Bytes of the tiles' counts.
+size_t sort_bytes(int64_t slots, int64_t experts) {
+  if (slots <= kDirectSlots) return 0;
+  return static_cast<size_t>(ceil_div(slots, tile_of(slots, experts))) * experts * sizeof(uint32_t);
+}
 
-// Waves below which a call spreads its tokens' columns over more of them.
-constexpr int64_t kFewWaves = 4096;
+// Rows' bytes from which they are read past the caches: larger ones leave nothing there
+// that would be found again.
+constexpr int64_t kStreamBytes = int64_t{64} << 20;
 
 template <typename TI, typename TO>
 int dispatch_run(const void* x, int64_t xstride, const int32_t* places, const float* weights,
                  int64_t n, int k, int64_t dim, int64_t rows, void* out, int64_t ostride,
                  hipStream_t stream) {
-  constexpr int VEC = cols_of<TI, TO>();
-  const bool few = n * ceil_div(dim, 64 * VEC * 4) < kFewWaves;
-  const int64_t parts = ceil_div(dim, 64 * VEC * (few ? 1 : 4));
-  return in_batches(n, kTokenBatch, [&](int64_t tokens, int64_t r) {
-    return launch(few ? dispatch_kernel<TI, TO, 1> : dispatch_kernel<TI, TO, 4>,
-                  dim3(static_cast<unsigned>(ceil_div(tokens, 4)), static_cast<unsigned>(parts)),
-                  dim3(256), stream, static_cast<const TI*>(x), xstride, places, weights, r, n, k,
-                  dim, rows, static_cast<TO*>(out), ostride);
+  const int parts = static_cast<int>(ceil_div(dim, 64 * cols_of<TI, TO>()));
+  return in_batches(n, ceil_div(kUnitBatch, parts), [&](int64_t tokens, int64_t r) {
+    return launch(dispatch_kernel<TI, TO>,
+                  dim3(static_cast<unsigned>(ceil_div(tokens * parts, 4))), dim3(256), stream,
+                  static_cast<const TI*>(x), xstride, places, weights, r,
+                  std::min(n, r + tokens), k, dim, parts, rows, static_cast<TO*>(out), ostride);
   });
 }
 
@@ -773,21 +763,24 @@ int combine_run(const void* y, int64_t ystride, int64_t rows, const int32_t* pla
                 hipStream_t stream) {
   constexpr int VEC = cols_of<TI, TO>();
   auto go = [&](auto kernel, int u) {
-    const int64_t parts = ceil_div(dim, 64 * VEC * u);
-    return in_batches(n, kTokenBatch, [&](int64_t tokens, int64_t r) {
-      return launch(kernel,
-                    dim3(static_cast<unsigned>(ceil_div(tokens, 4)),
-                         static_cast<unsigned>(parts)),
-                    dim3(256), stream, static_cast<const TI*>(y), ystride, rows, places, weights,
-                    r, n, k, dim, static_cast<TO*>(out), ostride);
+    const int parts = static_cast<int>(ceil_div(dim, 64 * VEC * u));
+    return in_batches(n, ceil_div(kUnitBatch, parts), [&](int64_t tokens, int64_t r) {
+      return launch(kernel, dim3(static_cast<unsigned>(ceil_div(tokens * parts, 4))), dim3(256),
+                    stream, static_cast<const TI*>(y), ystride, rows, places, weights, r,
+                    std::min(n, r + tokens), k, dim, parts, static_cast<TO*>(out), ostride);
     });
   };
-  const bool few = n * ceil_div(dim, 64 * VEC * 4) < kFewWaves;
-  if (k <= 2) return few ? go(combine_kernel<TI, TO, 1, 2, ACC>, 1)
-                         : go(combine_kernel<TI, TO, 4, 2, ACC>, 4);
-  if (k <= 4) return few ? go(combine_kernel<TI, TO, 1, 4, ACC>, 1)
-                         : go(combine_kernel<TI, TO, 2, 4, ACC>, 2);
-  return go(combine_kernel<TI, TO, 1, 8, ACC>, 1);
+  const bool past = n * k * dim * static_cast<int64_t>(sizeof(TI)) >= kStreamBytes;
+  const bool wide = dim >= 8 * 64 * VEC;
+#define GRZ_CALL(KB)                                                                      \
+  if (wide) return past ? go(combine_kernel<TI, TO, 4, KB, ACC, true>, 4)                 \
+                        : go(combine_kernel<TI, TO, 4, KB, ACC, false>, 4);               \
+  return past ? go(combine_kernel<TI, TO, 2, KB, ACC, true>, 2)                           \
+              : go(combine_kernel<TI, TO, 2, KB, ACC, false>, 2);
+  if (k <= 2) { GRZ_CALL(2) }
+  if (k <= 4) { GRZ_CALL(4) }
+  GRZ_CALL(8)
+#undef GRZ_CALL
 }
 
 template <typename TD, typename TY>
@@ -795,21 +788,20 @@ int combine_grad_run(const void* dout, int64_t dstride, const void* y, int64_t y
                      int64_t rows, const int32_t* places, const float* weights, int64_t n, int k,
                      int64_t dim, void* dy, int64_t dystride, float* dweights,
                      hipStream_t stream) {
-  auto go = [&](auto kernel, int w) {
+  auto go = [&](auto kernel) {
     return in_batches(n, kTokenBatch, [&](int64_t tokens, int64_t r) {
-      return launch(kernel, dim3(static_cast<unsigned>(ceil_div(tokens, 4 / w))), dim3(256),
-                    stream, static_cast<const TD*>(dout), dstride, static_cast<const TY*>(y),
-                    ystride, rows, places, weights, r, n, k, dim, static_cast<TY*>(dy), dystride,
-                    dweights);
+      return launch(kernel, dim3(static_cast<unsigned>(ceil_div(tokens * k, kGradWaves))),
+                    dim3(kGradWaves * 64), stream, static_cast<const TD*>(dout), dstride,
+                    static_cast<const TY*>(y), ystride, rows, places, weights, r,
+                    std::min(n, r + tokens), k, dim, static_cast<TY*>(dy), dystride, dweights);
     });
   };
-  const bool few = n < kFewWaves;
-  if (k <= 2) return few ? go(combine_grad_kernel<TD, TY, 2, 2, 4>, 4)
-                         : go(combine_grad_kernel<TD, TY, 2, 2, 1>, 1);
-  if (k <= 4) return few ? go(combine_grad_kernel<TD, TY, 1, 4, 4>, 4)
-                         : go(combine_grad_kernel<TD, TY, 1, 4, 1>, 1);
-  return few ? go(combine_grad_kernel<TD, TY, 1, 8, 4>, 4)
-             : go(combine_grad_kernel<TD, TY, 1, 8, 1>, 1);
+  const bool wide = dim > 4 * 64 * cols_of<TD, TY>();
+  if (n * k * dim * static_cast<int64_t>(sizeof(TY)) >= kStreamBytes)
+    return wide ? go(combine_grad_kernel<TD, TY, 8, true>)
+                : go(combine_grad_kernel<TD, TY, 4, true>);
+  return wide ? go(combine_grad_kernel<TD, TY, 8, false>)
+              : go(combine_grad_kernel<TD, TY, 4, false>);
 }
 
 }  // namespace
@@ -862,9 +854,7 @@ int dp_expert_route_grad(const void* logits, int dtype, int64_t n, int64_t exper
 
 size_t dp_expert_sort_workspace(int64_t n, int k, int64_t experts) {
   if (check_counts(n, k) != GRZ_OK || experts < 1 || experts > GRZ_MAX_EXPERTS) return 0;
-  const int64_t slots = n * k;
-  if (slots <= kDirectSlots) return 0;
-  return static_cast<size_t>(ceil_div(slots, tile_of(slots))) * experts * sizeof(uint32_t);
+  return sort_bytes(n * k, experts);
 }
 
 int dp_expert_sort(const void* ids, int id_bits, int64_t n, int k, int64_t experts,
@@ -877,7 +867,7 @@ int dp_expert_sort(const void* ids, int id_bits, int64_t n, int k, int64_t exper
   if (offsets == nullptr) return GRZ_EINVAL;
   if (!aligned(offsets, 4)) return GRZ_EALIGN;
   if ((st = check_slots(places, n, k)) != GRZ_OK) return st;
-  const size_t need = dp_expert_sort_workspace(n, k, experts);
+  const size_t need = sort_bytes(n * k, experts);
   if (need > 0) {
     if (workspace == nullptr) return GRZ_EINVAL;
     if (!aligned(workspace, 4)) return GRZ_EALIGN;
@@ -892,7 +882,7 @@ int dp_expert_sort(const void* ids, int id_bits, int64_t n, int k, int64_t exper
   a.slots = slots;
   a.experts = static_cast<int>(experts);
   a.bits = bits_of(a.experts);
-  a.tile = tile_of(slots);
+  a.tile = tile_of(slots, experts);
   a.tiles = static_cast<int>(slots > 0 ? ceil_div(slots, a.tile) : 1);
   a.counts = static_cast<uint32_t*>(workspace);
   a.offsets = offsets;
