@@ -28,7 +28,8 @@ constexpr int64_t kMaxPieces = int64_t{4096} * 4096 * 4096;  // of the norm's tr
 
 template <int LISTED> struct List {
   int count;
-  uint32_t first[LISTED + 1];  // the tensor's first piece in this launch
+  uint32_t pieces;         // of all its tensors
+  uint32_t first[LISTED];  // the tensor's first piece in this launch
   uint8_t type[LISTED];
   int64_t numel[LISTED];
   const void* data[LISTED];
@@ -50,30 +51,31 @@ struct ClipArgs {
 static_assert(sizeof(NormArgs) <= 4096 && sizeof(ClipArgs) <= 4096,
               "a launch's arguments exceed 4 KB");
 
-// The tensor that holds a piece: the last one whose first piece is not behind it.
+// The tensor that holds a piece: the last one whose first piece is not behind it.  All
+// first pieces are compared at once, one a lane: a launch's arguments come from far,
+// so a search of one dependent read after the other costs each wave microseconds.
 template <int LISTED>
-__device__ __forceinline__ int tensor_of(const List<LISTED>& l, uint32_t piece) {
-  int lo = 0, hi = l.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (l.first[mid] <= piece) lo = mid;
-    else hi = mid;
+__device__ __forceinline__ int tensor_of(const List<LISTED>& l, uint32_t piece, int lane) {
+  int t = -1;
+#pragma unroll
+  for (int b = 0; b < LISTED; b += 64) {
+    const int i = b + lane;
+    const bool there = i < LISTED && i < l.count && l.first[i < LISTED ? i : 0] <= piece;
+    t += __popcll(__ballot(there));
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(t);
 }
 
 // The wave's piece in its tensor.
 struct Piece {
   int tensor;
-  uint32_t number;  // in this launch
-  int64_t at;       // its first element
-  int64_t left;     // elements from there on
+  int64_t at;    // its first element
+  int64_t left;  // elements from there on
 };
 template <int LISTED>
-__device__ __forceinline__ Piece piece_of(const List<LISTED>& l, uint32_t number) {
+__device__ __forceinline__ Piece piece_of(const List<LISTED>& l, uint32_t number, int lane) {
   Piece p;
-  p.tensor = tensor_of(l, number);
-  p.number = number;
+  p.tensor = tensor_of(l, number, lane);
   p.at = static_cast<int64_t>(number - l.first[p.tensor]) * GRZ_PIECE;
   p.left = l.numel[p.tensor] - p.at;
   return p;
@@ -223,21 +225,24 @@ __global__ __launch_bounds__(256) void tensors_norm_kernel(const NormArgs a) {
   const int lane = threadIdx.x & 63;
   const uint32_t number =
       blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (number >= a.list.first[a.list.count]) return;
-  const Piece p = piece_of(a.list, number);
+  if (number >= a.list.pieces) return;
+  const Piece p = piece_of(a.list, number, lane);
   const double sum = a.stream ? piece_sum_of<true>(a, p, lane) : piece_sum_of<false>(a, p, lane);
   if (lane == 0) a.pieces[number] = sum;
 }
 
 // ---------------------------------------------------------------------------
-// Scaling, one wave a piece.
+// Scaling: one wave a run of kRun elements of a piece.
+
+constexpr int kRun = 1024, kRuns = GRZ_PIECE / kRun;
+constexpr int kClipWaves = 1;  // of a workgroup
 
 template <bool STREAM, typename TI, typename TO>
-__device__ __forceinline__ void scale_piece(const TI* p, TO* q, int64_t left, float scale,
-                                            int lane) {
+__device__ __forceinline__ void scale_run(const TI* p, TO* q, int64_t left, float scale,
+                                          int lane) {
   constexpr int E = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
-  constexpr int K = GRZ_PIECE / (64 * E);
-  if (left < GRZ_PIECE) {
+  constexpr int K = kRun / (64 * E);
+  if (left < kRun) {
     for (int e = lane; e < left; e += 64) put(q + e, widen(p[e]) * scale);
     return;
   }
@@ -274,35 +279,37 @@ __device__ __forceinline__ void scale_piece(const TI* p, TO* q, int64_t left, fl
 }
 
 template <bool STREAM>
-__device__ __forceinline__ void scale_piece_of(const ClipArgs& a, const Piece& p, float scale,
-                                               int lane) {
-  const void* in = a.list.data[p.tensor];
-  void* out = a.out[p.tensor];
-  const uint16_t* hi = static_cast<const uint16_t*>(in) + p.at;
-  const float* fi = static_cast<const float*>(in) + p.at;
-  uint16_t* ho = static_cast<uint16_t*>(out) + p.at;
-  float* fo = static_cast<float*>(out) + p.at;
-  if (a.list.type[p.tensor] == GRZ_BF16) {
-    if (a.out_type[p.tensor] == GRZ_BF16) scale_piece<STREAM>(hi, ho, p.left, scale, lane);
-    else scale_piece<STREAM>(hi, fo, p.left, scale, lane);
+__device__ __forceinline__ void scale_run_of(const ClipArgs& a, int tensor, int64_t at,
+                                             int64_t left, float scale, int lane) {
+  const void* in = a.list.data[tensor];
+  void* out = a.out[tensor];
+  const uint16_t* hi = static_cast<const uint16_t*>(in) + at;
+  const float* fi = static_cast<const float*>(in) + at;
+  uint16_t* ho = static_cast<uint16_t*>(out) + at;
+  float* fo = static_cast<float*>(out) + at;
+  if (a.list.type[tensor] == GRZ_BF16) {
+    if (a.out_type[tensor] == GRZ_BF16) scale_run<STREAM>(hi, ho, left, scale, lane);
+    else scale_run<STREAM>(hi, fo, left, scale, lane);
   } else {
-    if (a.out_type[p.tensor] == GRZ_BF16) scale_piece<STREAM>(fi, ho, p.left, scale, lane);
-    else scale_piece<STREAM>(fi, fo, p.left, scale, lane);
+    if (a.out_type[tensor] == GRZ_BF16) scale_run<STREAM>(fi, ho, left, scale, lane);
+    else scale_run<STREAM>(fi, fo, left, scale, lane);
   }
 }
 
-__global__ __launch_bounds__(256) void tensors_clip_kernel(const ClipArgs a) {
+__global__ __launch_bounds__(kClipWaves * 64) void tensors_clip_kernel(const ClipArgs a) {
   const int lane = threadIdx.x & 63;
-  const uint32_t number =
-      blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t pieces = a.list.first[a.list.count];
-  if (number >= pieces) return;
+  const uint32_t unit =
+      blockIdx.x * kClipWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t number = unit / kRuns;
+  if (number >= a.list.pieces) return;
   const float scale = a.scale != nullptr ? *a.scale : 1.0f;
-  const Piece p = piece_of(a.list, pieces - 1 - number);
+  const Piece p = piece_of(a.list, number, lane);
   // A gradient in its place that is scaled by 1 is what it was.
   if (scale == 1.0f && a.list.data[p.tensor] == a.out[p.tensor]) return;
-  if (a.stream) scale_piece_of<true>(a, p, scale, lane);
-  else scale_piece_of<false>(a, p, scale, lane);
+  const int skip = static_cast<int>(unit % kRuns) * kRun;
+  if (skip >= p.left) return;
+  if (a.stream) scale_run_of<true>(a, p.tensor, p.at + skip, p.left - skip, scale, lane);
+  else scale_run_of<false>(a, p.tensor, p.at + skip, p.left - skip, scale, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -328,6 +335,11 @@ int64_t pieces_of(const grz_tensor* t, int64_t count) {
   int64_t n = 0;
   for (int64_t i = 0; i < count; ++i) n += pieces_of(t[i].numel);
   return n;
+}
+
+// The pieces' sums and the levels of the tree over them.
+size_t workspace_of(int64_t pieces) {
+  return static_cast<size_t>(pieces) * sizeof(double) + dp_grad_sqnorm_workspace(pieces);
 }
 
 size_t bytes_of(const grz_tensor& t) { return static_cast<size_t>(t.numel) * elem_size(t.dtype); }
@@ -375,21 +387,21 @@ int check_apart(const grz_tensor* in, const grz_tensor* out, int64_t count) {
 
 // Bytes from which the tensors are streamed past the caches: what is much larger than
 // the 256 MB behind the L2s is not there any more when it is read again.
-constexpr int64_t kStreamBytes = int64_t{192} << 20;
+constexpr int64_t kStreamBytes = int64_t{96} << 20;
 
 // Appends tensors from `i` on to an empty list until it is full; returns the next one.
 template <int LISTED, typename F>
 int64_t fill(List<LISTED>& l, const grz_tensor* t, int64_t i, int64_t count, F also) {
   l.count = 0;
-  l.first[0] = 0;
+  l.pieces = 0;
   for (; i < count && l.count < LISTED; ++i) {
     if (t[i].numel == 0) continue;
     l.data[l.count] = t[i].data;
     l.numel[l.count] = t[i].numel;
     l.type[l.count] = static_cast<uint8_t>(t[i].dtype);
     also(l.count, i);
-    l.first[l.count + 1] = l.first[l.count] + static_cast<uint32_t>(pieces_of(t[i].numel));
-    ++l.count;
+    l.first[l.count++] = l.pieces;
+    l.pieces += static_cast<uint32_t>(pieces_of(t[i].numel));
   }
   return i;
 }
@@ -410,7 +422,7 @@ int64_t dp_tensor_pieces(const grz_tensor* tensors, int64_t count) {
 size_t dp_grad_sqnorm_tensors_workspace(const grz_tensor* tensors, int64_t count, int64_t lead) {
   const int64_t n = dp_tensor_pieces(tensors, count);
   if (n < 0 || lead < 0 || lead > kMaxPieces - n) return 0;
-  return static_cast<size_t>(n + lead) * sizeof(double) + dp_grad_sqnorm_workspace(n + lead);
+  return workspace_of(n + lead);
 }
 
 int dp_grad_sqnorm_tensors(const grz_tensor* tensors, int64_t count, double max_norm,
@@ -422,7 +434,7 @@ int dp_grad_sqnorm_tensors(const grz_tensor* tensors, int64_t count, double max_
   const int64_t n = pieces_of(tensors, count);
   if (lead < 0) return GRZ_EINVAL;
   if (lead > kMaxPieces - n) return GRZ_ERANGE;
-  const size_t need = dp_grad_sqnorm_tensors_workspace(tensors, count, lead);
+  const size_t need = workspace_of(n + lead);
   if (need > 0 && workspace == nullptr) return GRZ_EINVAL;
   if (sqnorm_out == nullptr && clip_scale_out == nullptr) return GRZ_EINVAL;
   if (!aligned(workspace, 8) || !aligned(sqnorm_out, 8) || !aligned(clip_scale_out, 4))
@@ -438,7 +450,7 @@ int dp_grad_sqnorm_tensors(const grz_tensor* tensors, int64_t count, double max_
   a.stream = bytes >= kStreamBytes;
   for (int64_t i = 0; i < count;) {
     i = fill(a.list, tensors, i, count, [](int, int64_t) {});
-    const uint32_t k = a.list.first[a.list.count];
+    const uint32_t k = a.list.pieces;
     if (k == 0) continue;
     st = launch(tensors_norm_kernel, dim3(static_cast<unsigned>(ceil_div(k, 4))), dim3(256),
                 stream, a);
@@ -469,10 +481,11 @@ int dp_grad_clip_tensors(const grz_tensor* grads, int64_t count, const float* cl
       a.out[to] = out[from].data;
       a.out_type[to] = static_cast<uint8_t>(out[from].dtype);
     });
-    const uint32_t k = a.list.first[a.list.count];
+    const uint32_t k = a.list.pieces;
     if (k == 0) continue;
-    st = launch(tensors_clip_kernel, dim3(static_cast<unsigned>(ceil_div(k, 4))), dim3(256),
-                stream, a);
+    st = launch(tensors_clip_kernel,
+                dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(k) * kRuns, kClipWaves))),
+                dim3(kClipWaves * 64), stream, a);
     if (st != GRZ_OK) return st;
   }
   return GRZ_OK;
