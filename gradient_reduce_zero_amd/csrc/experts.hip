@@ -63,21 +63,29 @@ template <typename T, int N> struct Cols {
   }
 };
 
-template <typename T, int N>
+template <bool STREAM> __device__ __forceinline__ void store_words(void* p, u32x4 v) {
+  u32x4e* q = static_cast<u32x4e*>(p);
+  if constexpr (STREAM) __builtin_nontemporal_store(v, q);
+  else *q = v;
+}
+template <bool STREAM> __device__ __forceinline__ void store_words(void* p, u32x2 v) {
+  u32x2e* q = static_cast<u32x2e*>(p);
+  if constexpr (STREAM) __builtin_nontemporal_store(v, q);
+  else *q = v;
+}
+
+template <typename T, int N, bool STREAM = true>
 __device__ __forceinline__ void store_cols(T* p, const float (&x)[N]) {
   if constexpr (sizeof(T) == 2) {
     uint32_t u[N / 2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i)
       u[i] = bf16_bits(x[2 * i]) | (bf16_bits(x[2 * i + 1]) << 16);
-    if constexpr (N == 8)
-      __builtin_nontemporal_store(u32x4e{u[0], u[1], u[2], u[3]}, reinterpret_cast<u32x4e*>(p));
-    else
-      __builtin_nontemporal_store(u32x2e{u[0], u[1]}, reinterpret_cast<u32x2e*>(p));
+    if constexpr (N == 8) store_words<STREAM>(p, u32x4{u[0], u[1], u[2], u[3]});
+    else store_words<STREAM>(p, u32x2{u[0], u[1]});
   } else {
-    __builtin_nontemporal_store(u32x4e{__float_as_uint(x[0]), __float_as_uint(x[1]),
-                                       __float_as_uint(x[2]), __float_as_uint(x[3])},
-                                reinterpret_cast<u32x4e*>(p));
+    store_words<STREAM>(p, u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                 __float_as_uint(x[2]), __float_as_uint(x[3])});
   }
 }
 
@@ -96,18 +104,17 @@ struct Unit {
   int64_t token;
   int part;
 };
-__device__ __forceinline__ Unit unit_of(int64_t row0, int parts) {
-  const uint32_t unit = blockIdx.x * 4 + wave_index();
+template <int WAVES> __device__ __forceinline__ Unit unit_of(int64_t row0, int parts) {
+  const uint32_t unit = blockIdx.x * WAVES + wave_index();
   const uint32_t token = unit / static_cast<uint32_t>(parts);
   return {row0 + token, static_cast<int>(unit - token * parts)};
 }
 
 // ---------------------------------------------------------------------------
 // The router.  A row of up to 1024 logits stays in the registers of G lanes (16,
-// four rows to a wave, or 64), V consecutive ones in each, so that every maximum
-// and sum is V operations and four (or six) lane exchanges.  The k largest come
-// one at a time: the row's largest key, the lowest lane that holds it, its lowest
-// element, which is then taken out.
+// four rows to a wave, or 64), V in each, so that every maximum and sum is V
+// operations and four (or six) lane exchanges.  The k largest come one at a time: the
+// row's largest key, the lowest element that has it, which is then taken out.
 
 // Keys ordered as the logits are: larger for larger, NaN above all, -0 as 0, and 0
 // for an element that is not there or taken out.
@@ -122,21 +129,36 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
+// A bf16 value's key is its upper half (the lower half is 0, or 0xffff below zero, and
+// is restored from its sign), which leaves room for the element's number, lower ones
+// first: one maximum then finds both (16384 x 256 bf16, k = 8: 9.2 us without).
+__device__ __forceinline__ uint32_t numbered(uint32_t key, int number) {
+  return (key & 0xffff0000u) | (0xffffu - static_cast<uint32_t>(number));
+}
+__device__ __forceinline__ uint32_t unnumbered(uint32_t key) {
+  return key & 0x80000000u ? key & 0xffff0000u : key | 0xffffu;
+}
 
 template <int CTRL> __device__ __forceinline__ uint32_t lane_swap_bits(uint32_t v) {
   return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
 }
 
-template <int G> __device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  v = max(v, lane_swap_bits<kSwap1>(v));
-  v = max(v, lane_swap_bits<kSwap2>(v));
-  v = max(v, lane_swap_bits<kHalfMirror>(v));
-  v = max(v, lane_swap_bits<kMirror>(v));
+template <int G, typename F> __device__ __forceinline__ uint32_t group_reduce(uint32_t v, F f) {
+  v = f(v, lane_swap_bits<kSwap1>(v));
+  v = f(v, lane_swap_bits<kSwap2>(v));
+  v = f(v, lane_swap_bits<kHalfMirror>(v));
+  v = f(v, lane_swap_bits<kMirror>(v));
   if constexpr (G == 64) {
     auto row = [&](int lane) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(v, lane)); };
-    v = max(max(row(0), row(16)), max(row(32), row(48)));
+    v = f(f(row(0), row(16)), f(row(32), row(48)));
   }
   return v;
+}
+template <int G> __device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  return group_reduce<G>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+template <int G> __device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  return group_reduce<G>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
 }
 template <int G> __device__ __forceinline__ float group_max(float v) {
   if constexpr (G == 64) return wave_max(v);
@@ -165,49 +187,109 @@ __device__ __forceinline__ float weight_of(float x, float m) {
   return x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((x - m) * kLog2e);
 }
 
-// The row's logits V * g .. V * g + V - 1, -inf behind the last.
-template <typename T, int V>
-__device__ __forceinline__ void load_logits(const T* row, int experts, int g, bool live,
-                                            float (&x)[V]) {
+// Which of the row's elements a lane of the group holds: runs of `kRun` (one access),
+// the group's runs side by side, so that each access of a wave is one run of memory a
+// row.
+template <typename T, int G, int V> struct Share {
+  static constexpr int kRun = V == 1 ? 1 : sizeof(T) == 2 && V >= 8 ? 8 : 4;
+  int g;
+  __device__ __forceinline__ int first(int h) const { return (h * G + g) * kRun; }
+  __device__ __forceinline__ int at(int i) const { return first(i / kRun) + i % kRun; }
+
+  // The elements, -inf behind the last.
+  __device__ __forceinline__ void load(const T* row, int experts, bool live,
+                                       float (&x)[V]) const {
 #pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = -INFINITY;
-  if (!live) return;
-  constexpr int E = sizeof(T) == 2 && V >= 8 ? 8 : 4;
-  const int c = g * V;
-  if (V >= 4 && c + V <= experts) {
-    if constexpr (V >= 4) {
+    for (int i = 0; i < V; ++i) x[i] = -INFINITY;
+    if (!live) return;
 #pragma unroll
-      for (int h = 0; h < V / E; ++h) {
-        Cols<T, E> y;
-        y.load(row + c + h * E);
+    for (int h = 0; h < V / kRun; ++h) {
+      const int c = first(h);
+      bool vector = false;
+      if constexpr (kRun > 1) {
+        vector = c + kRun <= experts;
+        if (vector) {
+          Cols<T, kRun> y;
+          y.load(row + c);
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[h * E + i] = y[i];
+          for (int i = 0; i < kRun; ++i) x[h * kRun + i] = y[i];
+        }
+      }
+      if (!vector) {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          if (c + i < experts) x[h * kRun + i] = widen(row[c + i]);
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (c + i < experts) x[i] = widen(row[c + i]);
   }
-}
+  __device__ __forceinline__ void store(T* row, int experts, const float (&x)[V]) const {
+#pragma unroll
+    for (int h = 0; h < V / kRun; ++h) {
+      const int c = first(h);
+      bool vector = false;
+      if constexpr (kRun > 1) {
+        vector = c + kRun <= experts;
+        if (vector) {
+          float y[kRun];
+#pragma unroll
+          for (int i = 0; i < kRun; ++i) y[i] = x[h * kRun + i];
+          store_cols<T, kRun, false>(row + c, y);
+        }
+      }
+      if (!vector) {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          if (c + i < experts) put(row + c + i, x[h * kRun + i]);
+      }
+    }
+  }
+};
 
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void route_kernel(const T* __restrict__ logits, int64_t stride,
                                                     int64_t row0, int64_t n, int experts, int k,
                                                     bool normalize, int32_t* __restrict__ ids,
                                                     float* __restrict__ weights) {
-  const int g = threadIdx.x & (G - 1);
+  const Share<T, G, V> share{static_cast<int>(threadIdx.x & (G - 1))};
+  const int g = share.g;
   const int64_t row = row0 + static_cast<int64_t>(blockIdx.x) * (256 / G) + threadIdx.x / G;
   const bool live = row < n;
   float x[V];
-  load_logits<T, V>(logits + (live ? row : 0) * stride, experts, g, live, x);
-  uint32_t key[V], best = 0;
+  share.load(logits + (live ? row : 0) * stride, experts, live, x);
+  constexpr bool kNumbered = sizeof(T) == 2;
+  uint32_t key[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    key[i] = live && g * V + i < experts ? key_of(x[i]) : 0u;
-    best = max(best, key[i]);
+    const int number = share.at(i);
+    key[i] = key_of(x[i]);
+    if constexpr (kNumbered) key[i] = numbered(key[i], number);
+    if (!live || number >= experts) key[i] = 0;
   }
-  uint32_t top = group_max<G>(best);
+  // The row's largest key; its element's number and, in `top`, its value's key.
+  auto next = [&](uint32_t& top) {
+    uint32_t best = 0, at = UINT32_MAX;
+#pragma unroll
+    for (int i = 0; i < V; ++i) best = max(best, key[i]);
+    best = group_max<G>(best);
+    if constexpr (kNumbered) {
+      at = 0xffffu - (best & 0xffffu);
+      top = unnumbered(best);
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = key[i] == best ? 0u : key[i];
+    } else {
+      top = best;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i)
+        if (key[i] == best) at = share.at(i);
+      at = group_min<G>(at);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (share.at(i) == static_cast<int>(at)) key[i] = 0;
+    }
+    return static_cast<int>(at);
+  };
+  uint32_t top;
+  int at = next(top);
   const bool open = top > kClosed;
   const float m = value_of(top);
   float total = 0.0f;
@@ -219,30 +301,11 @@ __global__ __launch_bounds__(256) void route_kernel(const T* __restrict__ logits
   int id = -1;
   float e = 0.0f;  // of the slot that the thread stores
   for (int j = 0; j < k; ++j) {
-    if (j > 0) {
-      best = 0;
-#pragma unroll
-      for (int i = 0; i < V; ++i) best = max(best, key[i]);
-      top = group_max<G>(best);
-    }
-    const uint64_t who = group_ballot<G>(best == top);
-    const int owner = __builtin_ctzll(who | (1ull << 63));
-    int at = 0;
-    if (g == owner) {
-      bool found = false;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const bool hit = key[i] == top && !found;
-        at = hit ? i : at;
-        key[i] = hit ? 0u : key[i];
-        found = found || hit;
-      }
-    }
-    at = __shfl(at, owner, G);
+    if (j > 0) at = next(top);
     const float p = top > kClosed ? weight_of(value_of(top), m) : 0.0f;
     if (normalize) total += p;
     if (g == j) {
-      id = top > kClosed ? owner * V + at : -1;
+      id = top > kClosed ? at : -1;
       e = p;
     }
   }
@@ -261,7 +324,8 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
     const int32_t* __restrict__ ids, const float* __restrict__ dweights, T* dlogits,
     int64_t dstride) {
   __shared__ float shares[256 / G][G * V];
-  const int g = threadIdx.x & (G - 1);
+  const Share<T, G, V> share_of{static_cast<int>(threadIdx.x & (G - 1))};
+  const int g = share_of.g;
   const int64_t row = row0 + static_cast<int64_t>(blockIdx.x) * (256 / G) + threadIdx.x / G;
   const bool live = row < n;
   const T* src = logits + (live ? row : 0) * stride;
@@ -276,13 +340,13 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
       xj = widen(src[id]);
     }
   }
-  float x[V], m, total = 0.0f, ej;
+  float x[V] = {}, m, total = 0.0f, ej;
   if (normalize) {
     m = group_max<G>(xj);
     ej = weight_of(xj, m);
     total = group_sum<G>(ej);
   } else {
-    load_logits<T, V>(src, experts, g, live, x);
+    share_of.load(src, experts, live, x);
     m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) m = fmaxf(m, x[i]);
@@ -300,7 +364,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
   const float share = id < 0 ? 0.0f : w * (normalize ? dw - both : dw);
   const bool some = group_ballot<G>(id >= 0 && dw != 0.0f) != 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) mine[g * V + i] = 0.0f;
+  for (int i = 0; i < V; ++i) mine[share_of.at(i)] = 0.0f;
   float sum = 0.0f;
   for (int j = 0; j < k; ++j) {
     const int other = __shfl(id, j, G);
@@ -311,31 +375,14 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
   if (id >= 0) mine[id] = sum;  // equal ids store the same sum
   wave_fence();
   if (!live) return;
-  T* dst = dlogits + row * dstride;
   float d[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    d[i] = mine[g * V + i];
+    d[i] = mine[share_of.at(i)];
     if (!normalize) d[i] -= total == 0.0f ? 0.0f : both * (x[i] / total);
     if (!some) d[i] = 0.0f;
   }
-  constexpr int E = sizeof(T) == 2 && V >= 8 ? 8 : 4;
-  const int c = g * V;
-  if (V >= 4 && c + V <= experts) {
-    if constexpr (V >= 4) {
-#pragma unroll
-      for (int h = 0; h < V / E; ++h) {
-        float y[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) y[i] = d[h * E + i];
-        store_cols<T, E>(dst + c + h * E, y);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (c + i < experts) put(dst + c + i, d[i]);
-  }
+  share_of.store(dlogits + row * dstride, experts, d);
 }
 
 // ---------------------------------------------------------------------------
@@ -479,14 +526,16 @@ __global__ __launch_bounds__(kSortThreads) void expert_place_kernel(SortArgs a) 
 // by one by the waves of the last run.
 
 // out[places[i][j]] = (weights[i][j]) x[i]: the row is read once and stored k times.
+constexpr int kDispatchWaves = 2;  // of a workgroup
+
 template <typename TI, typename TO>
-__global__ __launch_bounds__(256) void dispatch_kernel(
+__global__ __launch_bounds__(kDispatchWaves * 64) void dispatch_kernel(
     const TI* __restrict__ x, int64_t xstride, const int32_t* __restrict__ places,
     const float* __restrict__ weights, int64_t row0, int64_t n, int k, int64_t dim, int parts,
     int64_t rows, TO* __restrict__ out, int64_t ostride) {
   constexpr int VEC = cols_of<TI, TO>();
   const int lane = threadIdx.x & 63;
-  const auto [token, run] = unit_of(row0, parts);
+  const auto [token, run] = unit_of<kDispatchWaves>(row0, parts);
   if (token >= n) return;
   const TI* src = x + token * xstride;
   const int64_t whole = dim - dim % VEC;
@@ -513,14 +562,16 @@ __global__ __launch_bounds__(256) void dispatch_kernel(
 
 // out[i] = sum over j of (weights[i][j]) y[places[i][j]], added to out[i] with ACC:
 // KB rows' vectors on their way at once, summed in the slots' order.
+constexpr int kCombineWaves = 4;  // of a workgroup
+
 template <typename TI, typename TO, int U, int KB, bool ACC, bool STREAM>
-__global__ __launch_bounds__(256) void combine_kernel(
+__global__ __launch_bounds__(kCombineWaves * 64) void combine_kernel(
     const TI* __restrict__ y, int64_t ystride, int64_t rows, const int32_t* __restrict__ places,
     const float* __restrict__ weights, int64_t row0, int64_t n, int k, int64_t dim, int parts,
     TO* __restrict__ out, int64_t ostride) {
   constexpr int VEC = cols_of<TI, TO>();
   const int lane = threadIdx.x & 63;
-  const auto [token, run] = unit_of(row0, parts);
+  const auto [token, run] = unit_of<kCombineWaves>(row0, parts);
   if (token >= n) return;
   TO* dst = out + token * ostride;
   const int64_t whole = dim - dim % VEC;
@@ -683,6 +734,7 @@ template <typename F> int in_batches(int64_t n, int64_t batch, F f) {
   if (k <= 16 && experts <= 128) CALL(16, 8) \
   if (k <= 16 && experts <= 256) CALL(16, 16) \
   if (experts <= 256) CALL(64, 4)            \
+  if (experts <= 512) CALL(64, 8)            \
   CALL(64, 16)
 
 template <typename T>
@@ -751,7 +803,8 @@ int dispatch_run(const void* x, int64_t xstride, const int32_t* places, const fl
   const int parts = static_cast<int>(ceil_div(dim, 64 * cols_of<TI, TO>()));
   return in_batches(n, ceil_div(kUnitBatch, parts), [&](int64_t tokens, int64_t r) {
     return launch(dispatch_kernel<TI, TO>,
-                  dim3(static_cast<unsigned>(ceil_div(tokens * parts, 4))), dim3(256), stream,
+                  dim3(static_cast<unsigned>(ceil_div(tokens * parts, kDispatchWaves))),
+                  dim3(kDispatchWaves * 64), stream,
                   static_cast<const TI*>(x), xstride, places, weights, r,
                   std::min(n, r + tokens), k, dim, parts, rows, static_cast<TO*>(out), ostride);
   });
@@ -765,7 +818,8 @@ int combine_run(const void* y, int64_t ystride, int64_t rows, const int32_t* pla
   auto go = [&](auto kernel, int u) {
     const int parts = static_cast<int>(ceil_div(dim, 64 * VEC * u));
     return in_batches(n, ceil_div(kUnitBatch, parts), [&](int64_t tokens, int64_t r) {
-      return launch(kernel, dim3(static_cast<unsigned>(ceil_div(tokens * parts, 4))), dim3(256),
+      return launch(kernel, dim3(static_cast<unsigned>(ceil_div(tokens * parts, kCombineWaves))),
+                    dim3(kCombineWaves * 64),
                     stream, static_cast<const TI*>(y), ystride, rows, places, weights, r,
                     std::min(n, r + tokens), k, dim, parts, static_cast<TO*>(out), ostride);
     });
