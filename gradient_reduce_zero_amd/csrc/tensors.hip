@@ -22,8 +22,9 @@
 
 namespace {
 
-// Elements of all tensors of a call: their pieces' waves stay below 2^32 threads.
-constexpr int64_t kMaxElements = int64_t{1} << 37;
+constexpr int64_t kMaxElements = int64_t{1} << 37;  // of all tensors of a call
+// Pieces of one launch, whose threads stay below 2^32; longer lists take more launches.
+constexpr int64_t kLaunchPieces = int64_t{1} << 22;
 constexpr int64_t kMaxPieces = int64_t{4096} * 4096 * 4096;  // of the norm's tree
 
 template <int LISTED> struct List {
@@ -46,7 +47,6 @@ struct ClipArgs {
   uint8_t out_type[kListed];
   void* out[kListed];
   const float* scale;
-  bool stream;
 };
 static_assert(sizeof(NormArgs) <= 4096 && sizeof(ClipArgs) <= 4096,
               "a launch's arguments exceed 4 KB");
@@ -232,17 +232,17 @@ __global__ __launch_bounds__(256) void tensors_norm_kernel(const NormArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Scaling: one wave a run of kRun elements of a piece.
+// Scaling: a one-wave workgroup to a run of a piece, which leaves its CU as soon as its
+// own few accesses are done.
 
-constexpr int kRun = 1024, kRuns = GRZ_PIECE / kRun;
-constexpr int kClipWaves = 1;  // of a workgroup
+template <bool STREAM> constexpr int kRun = STREAM ? 1024 : 2048;  // elements
 
 template <bool STREAM, typename TI, typename TO>
 __device__ __forceinline__ void scale_run(const TI* p, TO* q, int64_t left, float scale,
                                           int lane) {
   constexpr int E = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
-  constexpr int K = kRun / (64 * E);
-  if (left < kRun) {
+  constexpr int K = kRun<STREAM> / (64 * E);
+  if (left < kRun<STREAM>) {
     for (int e = lane; e < left; e += 64) put(q + e, widen(p[e]) * scale);
     return;
   }
@@ -296,20 +296,17 @@ __device__ __forceinline__ void scale_run_of(const ClipArgs& a, int tensor, int6
   }
 }
 
-__global__ __launch_bounds__(kClipWaves * 64) void tensors_clip_kernel(const ClipArgs a) {
-  const int lane = threadIdx.x & 63;
-  const uint32_t unit =
-      blockIdx.x * kClipWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t number = unit / kRuns;
-  if (number >= a.list.pieces) return;
+template <bool STREAM>
+__global__ __launch_bounds__(64) void tensors_clip_kernel(const ClipArgs a) {
+  constexpr uint32_t kRuns = GRZ_PIECE / kRun<STREAM>;
+  const int lane = threadIdx.x;
   const float scale = a.scale != nullptr ? *a.scale : 1.0f;
-  const Piece p = piece_of(a.list, number, lane);
+  const Piece p = piece_of(a.list, blockIdx.x / kRuns, lane);
   // A gradient in its place that is scaled by 1 is what it was.
   if (scale == 1.0f && a.list.data[p.tensor] == a.out[p.tensor]) return;
-  const int skip = static_cast<int>(unit % kRuns) * kRun;
+  const int skip = static_cast<int>(blockIdx.x % kRuns) * kRun<STREAM>;
   if (skip >= p.left) return;
-  if (a.stream) scale_run_of<true>(a, p.tensor, p.at + skip, p.left - skip, scale, lane);
-  else scale_run_of<false>(a, p.tensor, p.at + skip, p.left - skip, scale, lane);
+  scale_run_of<STREAM>(a, p.tensor, p.at + skip, p.left - skip, scale, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -389,21 +386,32 @@ int check_apart(const grz_tensor* in, const grz_tensor* out, int64_t count) {
 // the 256 MB behind the L2s is not there any more when it is read again.
 constexpr int64_t kStreamBytes = int64_t{96} << 20;
 
-// Appends tensors from `i` on to an empty list until it is full; returns the next one.
+// Where a list goes on: element `at` (of a piece's beginning) of tensor `i`.
+struct Cursor {
+  int64_t i, at;
+};
+
+// Fills an empty list from there on until it or the launch is full.  `also`(entry,
+// tensor, element) adds what else the launch needs.
 template <int LISTED, typename F>
-int64_t fill(List<LISTED>& l, const grz_tensor* t, int64_t i, int64_t count, F also) {
+Cursor fill(List<LISTED>& l, const grz_tensor* t, Cursor c, int64_t count, F also) {
   l.count = 0;
   l.pieces = 0;
-  for (; i < count && l.count < LISTED; ++i) {
-    if (t[i].numel == 0) continue;
-    l.data[l.count] = t[i].data;
-    l.numel[l.count] = t[i].numel;
-    l.type[l.count] = static_cast<uint8_t>(t[i].dtype);
-    also(l.count, i);
-    l.first[l.count++] = l.pieces;
-    l.pieces += static_cast<uint32_t>(pieces_of(t[i].numel));
+  while (c.i < count && l.count < LISTED && l.pieces < kLaunchPieces) {
+    const int64_t left = t[c.i].numel - c.at;
+    const int64_t room = (kLaunchPieces - l.pieces) * GRZ_PIECE;
+    const int64_t take = left < room ? left : room;
+    if (take > 0) {
+      l.data[l.count] = static_cast<const char*>(t[c.i].data) + c.at * elem_size(t[c.i].dtype);
+      l.numel[l.count] = take;
+      l.type[l.count] = static_cast<uint8_t>(t[c.i].dtype);
+      also(l.count, c);
+      l.first[l.count++] = l.pieces;
+      l.pieces += static_cast<uint32_t>(pieces_of(take));
+    }
+    c = take < left ? Cursor{c.i, c.at + take} : Cursor{c.i + 1, 0};
   }
-  return i;
+  return c;
 }
 
 }  // namespace
@@ -448,8 +456,8 @@ int dp_grad_sqnorm_tensors(const grz_tensor* tensors, int64_t count, double max_
   NormArgs a;
   a.pieces = pieces + lead;
   a.stream = bytes >= kStreamBytes;
-  for (int64_t i = 0; i < count;) {
-    i = fill(a.list, tensors, i, count, [](int, int64_t) {});
+  for (Cursor c{0, 0}; c.i < count;) {
+    c = fill(a.list, tensors, c, count, [](int, const Cursor&) {});
     const uint32_t k = a.list.pieces;
     if (k == 0) continue;
     st = launch(tensors_norm_kernel, dim3(static_cast<unsigned>(ceil_div(k, 4))), dim3(256),
@@ -475,17 +483,18 @@ int dp_grad_clip_tensors(const grz_tensor* grads, int64_t count, const float* cl
   if ((st = check_apart(grads, out, count)) != GRZ_OK) return st;
   ClipArgs a;
   a.scale = clip_scale;
-  a.stream = bytes >= kStreamBytes;
-  for (int64_t i = 0; i < count;) {
-    i = fill(a.list, grads, i, count, [&](int to, int64_t from) {
-      a.out[to] = out[from].data;
-      a.out_type[to] = static_cast<uint8_t>(out[from].dtype);
+  const bool stream_past = bytes >= kStreamBytes;
+  for (Cursor c{0, 0}; c.i < count;) {
+    c = fill(a.list, grads, c, count, [&](int to, const Cursor& from) {
+      const grz_tensor& o = out[from.i];
+      a.out[to] = static_cast<char*>(o.data) + from.at * elem_size(o.dtype);
+      a.out_type[to] = static_cast<uint8_t>(o.dtype);
     });
     const uint32_t k = a.list.pieces;
     if (k == 0) continue;
-    st = launch(tensors_clip_kernel,
-                dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(k) * kRuns, kClipWaves))),
-                dim3(kClipWaves * 64), stream, a);
+    const auto grid = [&](int run) { return dim3(k * static_cast<unsigned>(GRZ_PIECE / run)); };
+    st = stream_past ? launch(tensors_clip_kernel<true>, grid(kRun<true>), dim3(64), stream, a)
+                     : launch(tensors_clip_kernel<false>, grid(kRun<false>), dim3(64), stream, a);
     if (st != GRZ_OK) return st;
   }
   return GRZ_OK;

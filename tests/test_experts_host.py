@@ -103,9 +103,12 @@ def test_sort_workspace():
     assert size(0, 1, 8) == 0 and size(64, 8, 128) == 0
     assert size(-1, 2, 8) == size(5, 0, 8) == size(5, 33, 8) == 0
     assert size(20000, 8, 0) == size(20000, 8, 1025) == size(2 ** 28 + 1, 1, 8) == 0
-    for n in (20000, 2 ** 20, 2 ** 23 + 1):
-        assert size(n, 8, 100) == 4 * 100 * len(range(0, n * 8, -(-n * 8 // 2 ** 18) * 1024))
-    assert size(2 ** 28, 1, 1024) == 2 ** 20
+    # Counts of every expert in tiles of a thousand slots or more, bounded whatever the
+    # slots.
+    for n, k in ((20000, 8), (2 ** 20, 8), (2 ** 23 + 1, 8), (2 ** 28, 1), (8193, 1)):
+        for experts in (1, 100, 1024):
+            tiles, rest = divmod(size(n, k, experts), 4 * experts)
+            assert rest == 0 and 0 < tiles <= -(-n * k // 1024) and tiles * experts <= 2 ** 18
 
 
 def test_overlaps():

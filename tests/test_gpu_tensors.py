@@ -202,6 +202,25 @@ def test_a_tensor_beyond_32_bit_offsets():
     assert norm_call([t], 0.0)[0] == 42.25
 
 
+def test_more_pieces_than_one_launch_takes():
+    # A launch ends inside the second tensor, at a piece's border (2^22 pieces).
+    n = 4096 * (2 ** 22 - 1) + 9000
+    a = torch.ones(10, device=DEV, dtype=BF16)
+    t = torch.zeros(n, device=DEV, dtype=BF16)
+    edge = 4096 * (2 ** 22 - 1)
+    t[edge - 1], t[edge], t[-1], t[0] = 3.0, 4.0, 12.0, 1.0
+    b = torch.full((5,), 2.0, device=DEV)
+    sq, scale, ws = norm_call([a, t, b], 7.0)
+    assert (sq, scale) == (200.0, torch.tensor(7.0 / math.sqrt(200.0)).item())
+    assert grz.dp_tensor_pieces([a, t, b]) == 2 ** 22 + 2 + 2
+    assert ws[2 ** 22 - 1].item() == 9.0 and ws[2 ** 22].item() == 16.0
+    assert ws[2 ** 22 + 2].item() == 144.0 and ws[2 ** 22 + 3].item() == 20.0
+    grz.dp_grad_clip_tensors([a, t, b], torch.tensor([0.5], device=DEV))
+    assert [t[i].item() for i in (edge - 1, edge, -1, 0)] == [1.5, 2.0, 6.0, 0.5]
+    assert (a == 0.5).all() and (b == 1.0).all()
+    assert norm_call([a, t, b], 0.0)[0] == 50.0
+
+
 def test_orders_of_dimensions_and_refused_layouts():
     a = torch.randn(30, 40, 5, device=DEV, generator=gen(10))
     ts = [a.permute(2, 0, 1), a.transpose(0, 1).contiguous().transpose(0, 1)[:, :, :]]
