@@ -9,8 +9,9 @@
 //   dp_expert_combine_grad  gradient of that sum: to the rows and to the weights
 //
 // All are bound by HBM or, where small, by their launches: at most three flops
-// per byte.  Integer atomics in LDS only, so every result bit is the same from run
-// to run.
+// per byte (the router apart, which its instructions bound).  Integer atomics in LDS
+// only, so every result bit is the same from run to run.  Times below are of one
+// MI355X.
 
 #include <hip/hip_runtime.h>
 
@@ -24,15 +25,16 @@
 
 namespace {
 
-constexpr int64_t kSlots = int64_t{1} << 28;      // n * k of one call
-constexpr int64_t kCols = int64_t{65535} * 64;    // columns: 2^16 column blocks of a launch
+constexpr int64_t kSlots = int64_t{1} << 28;       // n * k of one call
+constexpr int64_t kCols = int64_t{65535} * 64;     // columns of one call
 constexpr int64_t kTokenBatch = int64_t{1} << 20;  // tokens of one launch
 constexpr int64_t kUnitBatch = int64_t{1} << 23;   // their runs of columns, a wave each
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // ---------------------------------------------------------------------------
 // Vectors of a row that begin anywhere: gfx950 reads and writes 8 and 16 bytes at
-// any element's address, so rows need no alignment of their own.
+// any element's address, so rows need no alignment of their own (8000 x 1601 bf16 to
+// 4 experts, every row off the borders: 35.7 us for 128 MB, sort included).
 
 // N consecutive elements as they lie in memory (8 or 16 bytes), widened one by one
 // where they are used: many loads wait in few registers.
@@ -99,7 +101,8 @@ __device__ __forceinline__ int wave_index() {
 }
 
 // A wave's token and run of columns: the runs of a token's row are neighbours, so
-// that a row is read or written at one time.
+// that a row is read or written at one time (runs a launch's length apart: 16384 x
+// 4096 bf16 dispatched to 6 experts 205 instead of 177 us, combined 185 instead of 162).
 struct Unit {
   int64_t token;
   int part;
@@ -114,7 +117,9 @@ template <int WAVES> __device__ __forceinline__ Unit unit_of(int64_t row0, int p
 // The router.  A row of up to 1024 logits stays in the registers of G lanes (16,
 // four rows to a wave, or 64), V in each, so that every maximum and sum is V
 // operations and four (or six) lane exchanges.  The k largest come one at a time: the
-// row's largest key, the lowest element that has it, which is then taken out.
+// row's largest key, the lowest element that has it, which is then taken out.  Bound by
+// those rounds' instructions: 16384 x 128 bf16, k = 8: 5.4 us for 5 MB; 16384 x 256: 7.1
+// us bf16, 9.0 fp32.
 
 // Keys ordered as the logits are: larger for larger, NaN above all, -0 as 0, and 0
 // for an element that is not there or taken out.
@@ -189,7 +194,8 @@ __device__ __forceinline__ float weight_of(float x, float m) {
 
 // Which of the row's elements a lane of the group holds: runs of `kRun` (one access),
 // the group's runs side by side, so that each access of a wave is one run of memory a
-// row.
+// row (with V consecutive elements a lane the gradient of 16384 x 256 took 7.6 us bf16
+// and 14.9 fp32, instead of 6.1 and 6.4).
 template <typename T, int G, int V> struct Share {
   static constexpr int kRun = V == 1 ? 1 : sizeof(T) == 2 && V >= 8 ? 8 : 4;
   int g;
@@ -317,7 +323,9 @@ __global__ __launch_bounds__(256) void route_kernel(const T* __restrict__ logits
 
 // Lane j of a row's group takes slot j.  The slots' shares meet the row through
 // LDS, where each lane finds those of its elements; a token that lists an expert
-// twice has both slots add theirs up first, in the slots' order.
+// twice has both slots add theirs up first, in the slots' order.  Normalized weights
+// depend on the listed logits alone, so only those are read.  16384 x 256 bf16, k = 8:
+// 6.1 us, 7.4 not normalized (17 MB).
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void route_grad_kernel(
     const T* logits, int64_t stride, int64_t row0, int64_t n, int experts, int k, bool normalize,
@@ -393,9 +401,13 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
 // it, and `before` those of the tiles before its own.
 //
 //  - up to kDirectSlots one launch: each workgroup counts all slots itself, those
-//    before its tile and all, with integer atomics in LDS;
-//  - beyond that the tiles are counted by a first launch, at most kMaxTiles of
-//    them, and each workgroup adds their counts up.
+//    before its tile and all, with integer atomics in LDS (4096 slots of 64 experts
+//    4.9 us, 8192 5.8 against 6.8 by the next one, 16384 7.5 against 7.0; of 8 experts,
+//    whose counts collide more, 7.0 against 6.5 and 10.5 against 6.5);
+//  - beyond that the tiles are counted by a first launch and each workgroup adds all
+//    tiles' counts up (98304 slots of 64 experts 8.3 us).  At most kMaxTiles tiles, and
+//    at most kTileCounts counts, since everyone reads them (524288 slots of 1024
+//    experts: 24.6 us, 28.2 with 256 tiles, 30.7 with 64).
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
@@ -526,7 +538,11 @@ __global__ __launch_bounds__(kSortThreads) void expert_place_kernel(SortArgs a) 
 // by one by the waves of the last run.
 
 // out[places[i][j]] = (weights[i][j]) x[i]: the row is read once and stored k times.
-constexpr int kDispatchWaves = 2;  // of a workgroup
+// Bound by HBM, and by what 64 experts' rows written side by side cost it: 16384 x
+// 4096 bf16 to 6 experts of 64 147-160 us, 5.9-6.4 TB/s (places in the tokens' order
+// 8 % less).  Small workgroups free their slots one by one: 174 us a call with two waves,
+// 177 with four, 185 with eight; two or four vectors a lane 192 and 195.
+constexpr int kDispatchWaves = 2;
 
 template <typename TI, typename TO>
 __global__ __launch_bounds__(kDispatchWaves * 64) void dispatch_kernel(
@@ -561,8 +577,10 @@ __global__ __launch_bounds__(kDispatchWaves * 64) void dispatch_kernel(
 }
 
 // out[i] = sum over j of (weights[i][j]) y[places[i][j]], added to out[i] with ACC:
-// KB rows' vectors on their way at once, summed in the slots' order.
-constexpr int kCombineWaves = 4;  // of a workgroup
+// KB rows' vectors on their way at once, summed in the slots' order.  Bound by HBM:
+// 16384 x 4096 bf16 from 6 rows 155 us, 6.0 TB/s; 8011 x 1600 fp32 from 2, added, 31.6
+// us, 6.4 TB/s.
+constexpr int kCombineWaves = 4;
 
 template <typename TI, typename TO, int U, int KB, bool ACC, bool STREAM>
 __global__ __launch_bounds__(kCombineWaves * 64) void combine_kernel(
@@ -628,8 +646,10 @@ __global__ __launch_bounds__(kCombineWaves * 64) void combine_kernel(
 // y[places[i][j]]>: a wave to a slot, so that it streams one row of y and one of dy;
 // the token's other slots are its neighbours and find dout[i] in the caches.  U
 // vectors of each row on their way at once.  dy may be y: a lane stores where it has
-// read.
-constexpr int kGradWaves = 8;  // of a workgroup
+// read.  Bound by HBM, reads and writes mixed: 16384 x 4096 bf16 to 6 rows 324 us, 5.3
+// TB/s (places in the tokens' order 287; a wave a token with all its slots 363, four
+// waves 333); 8192 x 768 to 2 rows 12.5 us.
+constexpr int kGradWaves = 8;
 
 template <typename TD, typename TY, int U, bool STREAM>
 __global__ __launch_bounds__(kGradWaves * 64) void combine_grad_kernel(
@@ -727,7 +747,8 @@ template <typename F> int in_batches(int64_t n, int64_t batch, F f) {
 }
 
 // Lanes to a row and logits to a lane.  Sixteen lanes up to 256 experts and 16
-// slots: four rows share a wave's instructions.
+// slots: four rows share a wave's instructions (16384 x 512 rows, which do not, take
+// 13.9 us where 256 take 7.1).
 #define GRZ_ROUTE_SHAPES(CALL)               \
   if (k <= 16 && experts <= 16) CALL(16, 1)  \
   if (k <= 16 && experts <= 64) CALL(16, 4)  \
@@ -775,7 +796,6 @@ int check_route(const void* logits, int dtype, int64_t n, int64_t experts, int64
   return st != GRZ_OK ? st : check_matrix(logits, dtype, n, experts, stride);
 }
 
-// Every workgroup reads all tiles' counts, so many experts get fewer, longer tiles.
 int64_t tile_of(int64_t slots, int64_t experts) {
   if (slots <= kDirectSlots) return kSortThreads;
   const int64_t tiles = std::min(kMaxTiles, kTileCounts / experts);
@@ -792,8 +812,9 @@ size_t sort_bytes(int64_t slots, int64_t experts) {
   return static_cast<size_t>(ceil_div(slots, tile_of(slots, experts))) * experts * sizeof(uint32_t);
 }
 
-// Rows' bytes from which they are read past the caches: larger ones leave nothing there
-// that would be found again.
+// Rows' bytes from which they are read past the caches, since larger ones leave nothing
+// there that would be found again (102 MB combined: 32 us against 37.6, their gradient
+// 41 against 49; 25 MB: 9.9 against 9.1, 15.8 against 13.1).
 constexpr int64_t kStreamBytes = int64_t{64} << 20;
 
 template <typename TI, typename TO>
@@ -824,16 +845,22 @@ int combine_run(const void* y, int64_t ystride, int64_t rows, const int32_t* pla
                     std::min(n, r + tokens), k, dim, parts, static_cast<TO*>(out), ostride);
     });
   };
+  // Vectors a lane: one while that gives the chip few waves (32 x 4096 bf16, k = 8: 3.7 us
+  // with one, 5.2 with four; 1024 x 4096: 12.4 and 13.3), more of them then spare
+  // instructions (4096 x 768 bf16, k = 4: 5.5 us with one, 4.9 with two; 16384 x
+  // 4096, k = 6: 162 with one, 155 with four).
+  const int64_t units = n * ceil_div(dim, 64 * VEC);
   const bool past = n * k * dim * static_cast<int64_t>(sizeof(TI)) >= kStreamBytes;
   const bool wide = dim >= 8 * 64 * VEC;
-#define GRZ_CALL(KB)                                                                      \
+#define GRZ_CALL(KB, FEW)                                                                 \
+  if (units <= FEW) return go(combine_kernel<TI, TO, 1, KB, ACC, false>, 1);              \
   if (wide) return past ? go(combine_kernel<TI, TO, 4, KB, ACC, true>, 4)                 \
                         : go(combine_kernel<TI, TO, 4, KB, ACC, false>, 4);               \
   return past ? go(combine_kernel<TI, TO, 2, KB, ACC, true>, 2)                           \
               : go(combine_kernel<TI, TO, 2, KB, ACC, false>, 2);
-  if (k <= 2) { GRZ_CALL(2) }
-  if (k <= 4) { GRZ_CALL(4) }
-  GRZ_CALL(8)
+  if (k <= 2) { GRZ_CALL(2, 2048) }
+  if (k <= 4) { GRZ_CALL(4, 2048) }
+  GRZ_CALL(8, 8192)
 #undef GRZ_CALL
 }
 
@@ -850,6 +877,8 @@ int combine_grad_run(const void* dout, int64_t dstride, const void* y, int64_t y
                     std::min(n, r + tokens), k, dim, static_cast<TY*>(dy), dystride, dweights);
     });
   };
+  // Eight vectors a lane for rows that fill them (16384 x 4096 bf16, k = 6: 321 us, 326
+  // with four; 8000 x 1601, k = 4: 56 and 48).
   const bool wide = dim > 4 * 64 * cols_of<TD, TY>();
   if (n * k * dim * static_cast<int64_t>(sizeof(TY)) >= kStreamBytes)
     return wide ? go(combine_grad_kernel<TD, TY, 8, true>)

@@ -109,7 +109,9 @@ template <bool STREAM> __device__ __forceinline__ void store8(void* p, u32x2 v) 
 // fp64 in that order, then a balanced tree over each 64 threads and (w0 + w1) + (w2 +
 // w3).  A lane stands for four of those threads: with fp32 elements for t = lane +
 // 64 w (16 accesses of 16 bytes), with bf16 for t = 2 lane and 2 lane + 1 of each half
-// (8 accesses of 16 bytes), whose first addition is then its own.
+// (8 accesses of 16 bytes), whose first addition is then its own.  No barrier, all of
+// a piece on its way at once; bound by HBM: 1.04 G bf16 elements in 138 tensors 311 us,
+// 6.7 TB/s; 10.6 M in 48 tensors 7-8 us, latencies.
 
 template <int CTRL> __device__ __forceinline__ double add_swapped(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
@@ -233,7 +235,9 @@ __global__ __launch_bounds__(256) void tensors_norm_kernel(const NormArgs a) {
 
 // ---------------------------------------------------------------------------
 // Scaling: a one-wave workgroup to a run of a piece, which leaves its CU as soon as its
-// own few accesses are done.
+// own few accesses are done.  Bound by HBM: 1.04 G bf16 elements 660 us, 6.3 TB/s (four
+// waves 682; runs of 512 elements 736, of 2048 672, of 4096 708); 10.6 M, from the
+// caches in part: 10.2 us, 9.7 with runs of 2048.
 
 template <bool STREAM> constexpr int kRun = STREAM ? 1024 : 2048;  // elements
 
@@ -383,7 +387,8 @@ int check_apart(const grz_tensor* in, const grz_tensor* out, int64_t count) {
 }
 
 // Bytes from which the tensors are streamed past the caches: what is much larger than
-// the 256 MB behind the L2s is not there any more when it is read again.
+// the 256 MB behind the L2s is not there any more when it is read again (norm and clip of
+// 55 MB: 44.1 us, 45.8 streamed; of 184 MB 114 and 107, then 98 with one-wave runs).
 constexpr int64_t kStreamBytes = int64_t{96} << 20;
 
 // Where a list goes on: element `at` (of a piece's beginning) of tensor `i`.

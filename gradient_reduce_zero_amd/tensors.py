@@ -17,7 +17,7 @@ the current stream of the tensors' device (or ``stream``), and nothing synchroni
 the host.
 """
 
-import ctypes
+import functools
 
 import torch
 
@@ -35,8 +35,7 @@ class TensorList:
     def __init__(self, tensors):
         tensors = list(tensors)
         self.device = _device(tensors[0], "tensors[0]") if tensors else None
-        self.views, self.shapes = [], []
-        self.table = (N.Tensor * max(len(tensors), 1))()
+        self.views, entries = [], []
         for i, t in enumerate(tensors):
             if not isinstance(t, torch.Tensor) or t.get_device() != self.device:
                 _device(t, f"tensors[{i}]", self.device)
@@ -47,15 +46,19 @@ class TensorList:
                 raise ValueError(f"tensors[{i}]'s elements lie apart in memory or over each "
                                  f"other (shape {tuple(t.shape)}, strides {t.stride()})")
             self.views.append(t.detach())
-            self.shapes.append((t.shape, t.stride()))
-            entry = self.table[i]
-            entry.data, entry.numel, entry.dtype = t.data_ptr(), t.numel(), kind
-        self.pieces = lib().dp_tensor_pieces(self.table, len(tensors))
+            entries.append((t.data_ptr(), t.numel(), kind))
+        self.table = (N.Tensor * max(len(entries), 1))(*entries)
+        self.pieces = lib().dp_tensor_pieces(self.table, len(entries))
         if self.pieces < 0:
             check("dp_tensor_pieces", -self.pieces)
 
     def __len__(self):
         return len(self.views)
+
+    @functools.cached_property
+    def layouts(self):
+        """(shape, strides) of each tensor."""
+        return [(t.shape, t.stride()) for t in self.views]
 
 
 def _one_run(t):
@@ -125,8 +128,8 @@ def dp_grad_clip_tensors(tensors, clip_scale, out=None, stream=None):
     table = None
     if out is not None:
         out = _as_list(out)
-        if out.shapes != tensors.shapes:
-            _check_shapes(tensors, out)
+        if out.layouts != tensors.layouts:
+            _check_layouts(tensors, out)
         if out.device != tensors.device:
             raise ValueError("out is on another device than the tensors")
         table = out.table
@@ -137,10 +140,10 @@ def dp_grad_clip_tensors(tensors, clip_scale, out=None, stream=None):
           _scalar(clip_scale, "clip_scale", dev, torch.float32), table)
 
 
-def _check_shapes(tensors, out):
+def _check_layouts(tensors, out):
     if len(tensors) != len(out):
         raise ValueError(f"{len(tensors)} tensors, {len(out)} outputs")
-    for i, ((s, d), (so, do)) in enumerate(zip(tensors.shapes, out.shapes)):
+    for i, ((s, d), (so, do)) in enumerate(zip(tensors.layouts, out.layouts)):
         if s != so:
             raise ValueError(f"out[{i}] has shape {tuple(so)}, tensors[{i}] {tuple(s)}")
         # Strides count only where there is more than one element along them.

@@ -761,6 +761,8 @@ int dp_distill_grad(const void* logits, int dtype, int64_t n, int64_t vocab, int
  *  - Places that name rows twice are an error of the caller: such a row then holds
  *    one of its tokens' rows.  Nothing else is affected.
  *  - Rows that no place names are left as they were.
+ *  - Overlaps are judged by whole spans: what lies between a matrix's rows counts as
+ *    the matrix's.
  */
 
 /*
