@@ -296,7 +296,6 @@ __global__ __launch_bounds__(256) void route_kernel(const T* __restrict__ logits
   };
   uint32_t top;
   int at = next(top);
-  const bool open = top > kClosed;
   const float m = value_of(top);
   float total = 0.0f;
   if (!normalize) {
@@ -317,7 +316,7 @@ __global__ __launch_bounds__(256) void route_kernel(const T* __restrict__ logits
   }
   if (live && g < k) {
     ids[row * k + g] = id;
-    weights[row * k + g] = open ? e / total : 0.0f;
+    weights[row * k + g] = id >= 0 ? e / total : 0.0f;
   }
 }
 

@@ -758,8 +758,9 @@ int dp_distill_grad(const void* logits, int dtype, int64_t n, int64_t vocab, int
  *  - An id outside [0, experts) names no expert, a place outside [0, rows) no row:
  *    the slot adds nothing, is stored nowhere, and what its weight and dweight
  *    entries hold is not read.
- *  - Places that name rows twice are an error of the caller: such a row then holds
- *    one of its tokens' rows.  Nothing else is affected.
+ *  - Places that name a row twice are an error of the caller: what is written there
+ *    then holds elements of either token, and the dweights of its slots are
+ *    undefined where dy is y.  Nothing else is affected.
  *  - Rows that no place names are left as they were.
  *  - Overlaps are judged by whole spans: what lies between a matrix's rows counts as
  *    the matrix's.
@@ -777,7 +778,7 @@ int dp_distill_grad(const void* logits, int dtype, int64_t n, int64_t vocab, int
  * A logit of -inf closes an expert to the token: it is never listed, and where
  * fewer than k are open the last slots have id -1 and weight 0 (all of them in a
  * row with nothing open, a padded position).  A row that holds a NaN or +inf has
- * no softmax: its weights are NaN (its ids are still in order).
+ * no softmax: its listed experts' weights are NaN (the ids are still in order).
  * Errors: GRZ_EINVAL for k > experts; GRZ_ERANGE beyond GRZ_MAX_EXPERTS.
  */
 int dp_expert_route(const void* logits, int dtype, int64_t n, int64_t experts, int64_t stride,

@@ -46,8 +46,10 @@ class Route:
         # relative error of the sum: each term's, and the additions one takes part in
         depth = 16 + 6 + 2 if not normalize else ids.shape[1]
         tol_s = ((ep * (3 * d(pool) + 2)).sum(1, keepdim=True) / self.s + depth) * U
-        self.w = torch.where(listed == -math.inf, torch.zeros_like(listed),
-                             torch.exp(listed - m)) / self.s
+        # a slot without an expert weighs 0, in a row without a softmax too
+        self.w = torch.where(self.ok, torch.where(listed == -math.inf, torch.zeros_like(listed),
+                                                  torch.exp(listed - m)) / self.s,
+                             torch.zeros_like(listed))
         self.rel = (3 * d(listed) + 2) * U + tol_s + U
         self.tol = self.w * self.rel * 1.01 + TINY
         if not normalize:

@@ -298,6 +298,29 @@ def test_many_tokens(n, k, dim, dtype):
     assert torch.equal(dy[places.long()], (back[:, None, :] * w[:, :, None]).to(dtype))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_named_twice_harm_no_others(dtype):
+    n, k, d = 300, 3, 700
+    places = torch.randperm(n * k, generator=torch.Generator().manual_seed(5)).int().view(n, k)
+    twice = places[7, 1].item()
+    places[200, 2] = twice
+    places = places.to(DEV)
+    x, _ = matrix(n, d, dtype, seed=55)
+    out = torch.zeros(n * k, d, device=DEV, dtype=dtype)
+    grz.dp_expert_dispatch(x, places, out)
+    want = ref.dispatch(x, places, None, torch.zeros_like(out))
+    others = torch.arange(n * k) != twice
+    assert torch.equal(out.cpu()[others], want[others])
+    both = torch.stack([x[7], x[200]]).cpu()
+    assert ((out[twice].cpu() == both[0]) | (out[twice].cpu() == both[1])).all()
+    dw = torch.empty(n, k, device=DEV)
+    want, dwant, tol = ref.combine_grad(x, out, places, None, torch.zeros_like(out))
+    dy = torch.zeros_like(out)
+    grz.dp_expert_combine_grad(x, out, places, None, dy=dy, dweights=dw)
+    assert torch.equal(dy.cpu()[others], want[others])
+    assert_close(dw, dwant, tol, "dweights")
+
+
 def test_weights_of_zero_infinity_and_nan():
     # A slot counts by its place: a weight of 0 times an infinity is a NaN, as written.
     places = torch.tensor([[0, 1], [2, -1]], device=DEV, dtype=I32)
