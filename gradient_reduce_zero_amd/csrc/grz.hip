@@ -563,10 +563,19 @@ __attribute__((amdgpu_waves_per_eu(WAVES, WAVES))) void rs_mean_kernel(const RsA
 __device__ __forceinline__ double fan_block_sum(const double* __restrict__ x, int64_t n,
                                                 int64_t base, double* lds) {
   double s = 0.0;
+  if (base < n) {
+    constexpr int kPer = kReduceFan / kThreads;
+    double v[kPer];
+    // Every read is of x, so all go out at once (4096 values 2.5 us, 3.7 with each read
+    // only where it counts; two levels over 254,000 5.0 and 6.2).
 #pragma unroll
-  for (int k = 0; k < kReduceFan / kThreads; ++k) {
-    const int64_t i = base + k * kThreads + threadIdx.x;
-    if (i < n) s += x[i];
+    for (int k = 0; k < kPer; ++k) {
+      const int64_t i = base + k * kThreads + threadIdx.x;
+      v[k] = x[i < n ? i : base];
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (base + k * kThreads + threadIdx.x < n) s += v[k];
   }
   return block_sum_fixed(s, lds);
 }
