@@ -39,7 +39,6 @@ struct NormArgs {
   static constexpr int kListed = 184;
   List<kListed> list;
   double* pieces;
-  bool stream;
 };
 struct ClipArgs {
   static constexpr int kListed = 128;
@@ -103,15 +102,60 @@ template <bool STREAM> __device__ __forceinline__ void store8(void* p, u32x2 v) 
   else *q = v;
 }
 
+// WORDS words of the elements from `e` on, 0 where not all of them are among the first
+// `left` (FULL: all are, and nothing is asked, which keeps the loads of a piece
+// together: 1.04 G elements' norm 311 us instead of 341, clip 665 instead of 695).
+template <bool STREAM, bool FULL, int WORDS, typename T>
+__device__ __forceinline__ auto load_whole(const T* p, int e, int64_t left) {
+  uint32_t __attribute__((ext_vector_type(WORDS))) u = {};
+  if (FULL || e + WORDS * 4 / static_cast<int>(sizeof(T)) <= left) {
+    if constexpr (WORDS == 4) u = load16<STREAM>(p + e);
+    else u = load8<STREAM>(p + e);
+  }
+  return u;
+}
+
+// The elements behind the last whole vector of N, read one a lane (one after the other
+// by the lane whose vector they are, they take microseconds).
+template <typename T, int N> struct Rest {
+  int at, count;
+  T mine;
+  __device__ __forceinline__ Rest(const T* p, int64_t left, int lane) {
+    const int n = left < GRZ_PIECE ? static_cast<int>(left) : GRZ_PIECE;
+    count = n % N;
+    at = n - count;
+    mine = lane < count ? p[at + lane] : T{};
+  }
+  // Puts them where a lane holds the vector that begins at `at`.
+  template <typename V> __device__ __forceinline__ void into(V& u, int e) const {
+    if (count == 0) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint32_t bits;
+      if constexpr (sizeof(T) == 2)
+        bits = static_cast<uint32_t>(__builtin_amdgcn_readlane(mine, i)) << (16 * (i & 1));
+      else
+        bits = __builtin_amdgcn_readlane(__float_as_uint(mine), i);
+      if (e == at) u[i * static_cast<int>(sizeof(T)) / 4] |= bits;
+    }
+  }
+};
+
 // ---------------------------------------------------------------------------
-// Piece sums, one wave a piece.  Their bits are those of the reduce's piece sums:
-// thread t of 256 takes elements 1024 k + 4 t .. + 3 for k = 0 .. 3, squares added in
-// fp64 in that order, then a balanced tree over each 64 threads and (w0 + w1) + (w2 +
-// w3).  A lane stands for four of those threads: with fp32 elements for t = lane +
-// 64 w (16 accesses of 16 bytes), with bf16 for t = 2 lane and 2 lane + 1 of each half
-// (8 accesses of 16 bytes), whose first addition is then its own.  No barrier, all of
-// a piece on its way at once; bound by HBM: 1.04 G bf16 elements in 138 tensors 311 us,
-// 6.7 TB/s; 10.6 M in 48 tensors 7-8 us, latencies.
+// Piece sums.  Their bits are those of the reduce's piece sums: thread t of 256 takes
+// elements 1024 k + 4 t .. + 3 for k = 0 .. 3, squares added in fp64 in that order,
+// then a balanced tree over each 64 threads and (w0 + w1) + (w2 + w3).  Elements behind
+// a tensor's last count as 0, which changes no sum of squares.
+//
+//  - Many pieces: a wave a piece, without a barrier, all of it on its way at once.  A
+//    lane stands for four of those threads: with fp32 elements for t = lane + 64 w (16
+//    accesses of 16 bytes), with bf16 for t = 2 lane and 2 lane + 1 of each half (8 of
+//    16 bytes), whose first addition is then its own.  Bound by HBM: 1.04 G bf16
+//    elements in 138 tensors 311 us, 6.7 TB/s.
+//  - Few: a workgroup a piece, which shortens each wave's chain of conversions and
+//    additions (when first built, norms of 10.6 M elements 11.8 us bf16 and 13.5 fp32
+//    against 16.1 and 20.3, of 24 M bf16 16.0 against 16.7, of 100 M 56 against 38; now
+//    9.4 and 11.4, the tree's launch of 2.6 included).
 
 template <int CTRL> __device__ __forceinline__ double add_swapped(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
@@ -127,140 +171,166 @@ __device__ __forceinline__ double lane_of(double v, int lane) {
   const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(b >> 32), lane);
   return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
-// Sums over each row of 16 lanes, in all of them.
-__device__ __forceinline__ double row_sum(double v) {
+// The wave's sum, lane by lane from neighbours outwards.
+__device__ __forceinline__ double wave_sum(double v) {
   v = add_swapped<kSwap1>(v);
   v = add_swapped<kSwap2>(v);
   v = add_swapped<kHalfMirror>(v);
-  return add_swapped<kMirror>(v);
+  v = add_swapped<kMirror>(v);
+  return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 
 __device__ __forceinline__ void add_square(double& s, float x) {
   s = __fma_rn(static_cast<double>(x), static_cast<double>(x), s);
 }
-
-template <bool STREAM>
-__device__ __forceinline__ double piece_sum(const uint16_t* p, int64_t left, int lane) {
-  double s[2][2] = {};  // [half of the threads][thread of the lane's pair]
-  if (left >= GRZ_PIECE) {
-    u32x4 u[4][2];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        u[k][h] = load16<STREAM>(p + 1024 * k + 512 * h + 8 * lane);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          add_square(s[h][i >> 1], __uint_as_float(u[k][h][i] << 16));
-          add_square(s[h][i >> 1], __uint_as_float(u[k][h][i] & 0xffff0000u));
-        }
+// A word's squares: one fp32 element's or two bf16 ones'.
+template <typename T> __device__ __forceinline__ void add_squares(double& s, uint32_t word) {
+  if constexpr (sizeof(T) == 2) {
+    add_square(s, __uint_as_float(word << 16));
+    add_square(s, __uint_as_float(word & 0xffff0000u));
   } else {
+    add_square(s, __uint_as_float(word));
+  }
+}
+
+template <bool STREAM, bool FULL>
+__device__ __forceinline__ double piece_sum(const uint16_t* p, int64_t left, int lane) {
+  u32x4 u[4][2];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      u[k][h] = load_whole<STREAM, FULL, 4>(p, 1024 * k + 512 * h + 8 * lane, left);
+  if constexpr (!FULL) {
+    const Rest<uint16_t, 8> rest(p, left, lane);
+#pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = 1024 * k + 512 * h + 8 * lane + i;
-          if (e < left) add_square(s[h][i >> 2], widen(p[e]));
-        }
+      for (int h = 0; h < 2; ++h) rest.into(u[k][h], 1024 * k + 512 * h + 8 * lane);
   }
   double w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    double v = s[h][0] + s[h][1];
-    v = add_swapped<kSwap1>(v);
-    v = add_swapped<kSwap2>(v);
-    v = add_swapped<kHalfMirror>(v);
-    v = add_swapped<kMirror>(v);
-    w[h] = (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+    double s[2] = {};  // of the lane's two threads
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add_squares<uint16_t>(s[i >> 1], u[k][h][i]);
+    // Lanes 0 .. 31 hold one wave's threads, 32 .. 63 the next one's.
+    w[h] = wave_sum(s[0] + s[1]);
   }
   return w[0] + w[1];
 }
 
-template <bool STREAM>
+template <bool STREAM, bool FULL>
 __device__ __forceinline__ double piece_sum(const float* p, int64_t left, int lane) {
-  double s[4] = {};
-  if (left >= GRZ_PIECE) {
-    u32x4 u[4][4];
+  u32x4 u[4][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      u[k][w] = load_whole<STREAM, FULL, 4>(p, 1024 * k + 256 * w + 4 * lane, left);
+  if constexpr (!FULL) {
+    const Rest<float, 4> rest(p, left, lane);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        u[k][w] = load16<STREAM>(p + 1024 * k + 256 * w + 4 * lane);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) add_square(s[w], __uint_as_float(u[k][w][i]));
-  } else {
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = 1024 * k + 256 * w + 4 * lane + i;
-          if (e < left) add_square(s[w], p[e]);
-        }
+      for (int w = 0; w < 4; ++w) rest.into(u[k][w], 1024 * k + 256 * w + 4 * lane);
   }
+  double s[4] = {};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const double v = row_sum(s[w]);
-    s[w] = (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add_squares<float>(s[w], u[k][w][i]);
+    s[w] = wave_sum(s[w]);
   }
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-template <bool STREAM>
+template <bool STREAM, bool FULL>
 __device__ __forceinline__ double piece_sum_of(const NormArgs& a, const Piece& p, int lane) {
   const void* data = a.list.data[p.tensor];
   return a.list.type[p.tensor] == GRZ_BF16
-             ? piece_sum<STREAM>(static_cast<const uint16_t*>(data) + p.at, p.left, lane)
-             : piece_sum<STREAM>(static_cast<const float*>(data) + p.at, p.left, lane);
+             ? piece_sum<STREAM, FULL>(static_cast<const uint16_t*>(data) + p.at, p.left, lane)
+             : piece_sum<STREAM, FULL>(static_cast<const float*>(data) + p.at, p.left, lane);
 }
 
-__global__ __launch_bounds__(256) void tensors_norm_kernel(const NormArgs a) {
+template <bool STREAM> __global__ __launch_bounds__(256) void tensors_norm_kernel(
+    const NormArgs a) {
   const int lane = threadIdx.x & 63;
   const uint32_t number =
       blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (number >= a.list.pieces) return;
   const Piece p = piece_of(a.list, number, lane);
-  const double sum = a.stream ? piece_sum_of<true>(a, p, lane) : piece_sum_of<false>(a, p, lane);
+  const double sum = p.left >= GRZ_PIECE ? piece_sum_of<STREAM, true>(a, p, lane)
+                                         : piece_sum_of<STREAM, false>(a, p, lane);
   if (lane == 0) a.pieces[number] = sum;
+}
+
+// The sum of the wave's 64 of the 256 threads.
+template <bool FULL, typename T>
+__device__ __forceinline__ double quarter_sum(const T* p, int64_t left) {
+  constexpr int W = sizeof(T);  // words of four elements
+  const int t = threadIdx.x;
+  uint32_t __attribute__((ext_vector_type(W))) u[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) u[k] = load_whole<false, FULL, W>(p, 1024 * k + 4 * t, left);
+  if constexpr (!FULL) {
+    const Rest<T, 4> rest(p, left, t & 63);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) rest.into(u[k], 1024 * k + 4 * t);
+  }
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < W; ++i) add_squares<T>(s, u[k][i]);
+  return wave_sum(s);
+}
+
+constexpr uint32_t kFewPieces = 6144;
+
+__global__ __launch_bounds__(256) void tensors_norm_few_kernel(const NormArgs a) {
+  __shared__ double sums[4];
+  const Piece p = piece_of(a.list, blockIdx.x, threadIdx.x & 63);
+  const void* data = a.list.data[p.tensor];
+  const uint16_t* h = static_cast<const uint16_t*>(data) + p.at;
+  const float* f = static_cast<const float*>(data) + p.at;
+  const bool half = a.list.type[p.tensor] == GRZ_BF16;
+  const double s = p.left >= GRZ_PIECE
+                       ? (half ? quarter_sum<true>(h, p.left) : quarter_sum<true>(f, p.left))
+                       : (half ? quarter_sum<false>(h, p.left) : quarter_sum<false>(f, p.left));
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) a.pieces[blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
 // ---------------------------------------------------------------------------
 // Scaling: a one-wave workgroup to a run of a piece, which leaves its CU as soon as its
 // own few accesses are done.  Bound by HBM: 1.04 G bf16 elements 660 us, 6.3 TB/s (four
 // waves 682; runs of 512 elements 736, of 2048 672, of 4096 708); 10.6 M, from the
-// caches in part: 10.2 us, 9.7 with runs of 2048.
+// caches in part: 10.2 us, 9.5 with runs of 2048.
 
 template <bool STREAM> constexpr int kRun = STREAM ? 1024 : 2048;  // elements
 
-template <bool STREAM, typename TI, typename TO>
+template <bool STREAM, bool FULL, typename TI, typename TO>
 __device__ __forceinline__ void scale_run(const TI* p, TO* q, int64_t left, float scale,
                                           int lane) {
   constexpr int E = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
   constexpr int K = kRun<STREAM> / (64 * E);
-  if (left < kRun<STREAM>) {
-    for (int e = lane; e < left; e += 64) put(q + e, widen(p[e]) * scale);
-    return;
-  }
   constexpr int IW = E * sizeof(TI) / 4, OW = E * sizeof(TO) / 4;  // words of an access
-  using In = uint32_t __attribute__((ext_vector_type(IW)));
-  using Out = uint32_t __attribute__((ext_vector_type(OW)));
-  In u[K];
+  uint32_t __attribute__((ext_vector_type(IW))) u[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if constexpr (IW == 4) u[k] = load16<STREAM>(p + 64 * E * k + E * lane);
-    else u[k] = load8<STREAM>(p + 64 * E * k + E * lane);
+  for (int k = 0; k < K; ++k) u[k] = load_whole<STREAM, FULL, IW>(p, 64 * E * k + E * lane, left);
+  if constexpr (!FULL) {  // the elements behind the last whole vector, one a lane
+    const int behind = static_cast<int>(left - left % E) + lane;
+    if (behind < left) put(q + behind, widen(p[behind]) * scale);
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
+    const int e = 64 * E * k + E * lane;
     float x[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -269,20 +339,19 @@ __device__ __forceinline__ void scale_run(const TI* p, TO* q, int64_t left, floa
       else
         x[i] = __uint_as_float(u[k][i]) * scale;
     }
-    Out o;
-    if constexpr (sizeof(TO) == 2) {
+    if (!FULL && e + E > left) continue;
+    uint32_t __attribute__((ext_vector_type(OW))) o;
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) o[i] = bf16_bits(x[2 * i]) | bf16_bits(x[2 * i + 1]) << 16;
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) o[i] = __float_as_uint(x[i]);
+    for (int i = 0; i < OW; ++i) {
+      if constexpr (sizeof(TO) == 2) o[i] = bf16_bits(x[2 * i]) | bf16_bits(x[2 * i + 1]) << 16;
+      else o[i] = __float_as_uint(x[i]);
     }
-    if constexpr (OW == 4) store16<STREAM>(q + 64 * E * k + E * lane, o);
-    else store8<STREAM>(q + 64 * E * k + E * lane, o);
+    if constexpr (OW == 4) store16<STREAM>(q + e, o);
+    else store8<STREAM>(q + e, o);
   }
 }
 
-template <bool STREAM>
+template <bool STREAM, bool FULL>
 __device__ __forceinline__ void scale_run_of(const ClipArgs& a, int tensor, int64_t at,
                                              int64_t left, float scale, int lane) {
   const void* in = a.list.data[tensor];
@@ -292,11 +361,11 @@ __device__ __forceinline__ void scale_run_of(const ClipArgs& a, int tensor, int6
   uint16_t* ho = static_cast<uint16_t*>(out) + at;
   float* fo = static_cast<float*>(out) + at;
   if (a.list.type[tensor] == GRZ_BF16) {
-    if (a.out_type[tensor] == GRZ_BF16) scale_run<STREAM>(hi, ho, left, scale, lane);
-    else scale_run<STREAM>(hi, fo, left, scale, lane);
+    if (a.out_type[tensor] == GRZ_BF16) scale_run<STREAM, FULL>(hi, ho, left, scale, lane);
+    else scale_run<STREAM, FULL>(hi, fo, left, scale, lane);
   } else {
-    if (a.out_type[tensor] == GRZ_BF16) scale_run<STREAM>(fi, ho, left, scale, lane);
-    else scale_run<STREAM>(fi, fo, left, scale, lane);
+    if (a.out_type[tensor] == GRZ_BF16) scale_run<STREAM, FULL>(fi, ho, left, scale, lane);
+    else scale_run<STREAM, FULL>(fi, fo, left, scale, lane);
   }
 }
 
@@ -310,7 +379,9 @@ __global__ __launch_bounds__(64) void tensors_clip_kernel(const ClipArgs a) {
   if (scale == 1.0f && a.list.data[p.tensor] == a.out[p.tensor]) return;
   const int skip = static_cast<int>(blockIdx.x % kRuns) * kRun<STREAM>;
   if (skip >= p.left) return;
-  scale_run_of<STREAM>(a, p.tensor, p.at + skip, p.left - skip, scale, lane);
+  const int64_t at = p.at + skip, left = p.left - skip;
+  if (left >= kRun<STREAM>) scale_run_of<STREAM, true>(a, p.tensor, at, left, scale, lane);
+  else scale_run_of<STREAM, false>(a, p.tensor, at, left, scale, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -460,13 +531,14 @@ int dp_grad_sqnorm_tensors(const grz_tensor* tensors, int64_t count, double max_
   double* const pieces = static_cast<double*>(workspace);
   NormArgs a;
   a.pieces = pieces + lead;
-  a.stream = bytes >= kStreamBytes;
   for (Cursor c{0, 0}; c.i < count;) {
     c = fill(a.list, tensors, c, count, [](int, const Cursor&) {});
     const uint32_t k = a.list.pieces;
     if (k == 0) continue;
-    st = launch(tensors_norm_kernel, dim3(static_cast<unsigned>(ceil_div(k, 4))), dim3(256),
-                stream, a);
+    st = k <= kFewPieces
+             ? launch(tensors_norm_few_kernel, dim3(k), dim3(256), stream, a)
+             : launch(bytes >= kStreamBytes ? tensors_norm_kernel<true> : tensors_norm_kernel<false>,
+                      dim3(static_cast<unsigned>(ceil_div(k, 4))), dim3(256), stream, a);
     if (st != GRZ_OK) return st;
     a.pieces += k;
   }
