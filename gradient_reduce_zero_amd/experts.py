@@ -31,13 +31,18 @@ from ._native import lib
 from .tokens import _F32, _I32, _call, _device, _ids, _list, _rows
 
 
-def _slots(t, name):
-    """(n, k) of an array of slots."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected tokens x slots")
-    return t.shape
+def _slots(t, name, dev, dtype, n):
+    """(pointer, k) of a contiguous array of ``n`` tokens' slots."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _device(t, name, dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != n:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected ({n}, any)")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), shape[1]
 
 
 def dp_expert_route(logits, ids, weights, normalize=False, stream=None):
@@ -47,10 +52,9 @@ def dp_expert_route(logits, ids, weights, normalize=False, stream=None):
     logit is -inf are closed: slots left over have id -1 and weight 0."""
     dev = _device(logits, "logits")
     lp, lt, n, experts, ls = _rows(logits, "logits", dev)
-    k = _slots(ids, "ids")[1]
+    ip, k = _slots(ids, "ids", dev, _I32, n)
     _call("dp_expert_route", dev, stream, lp, lt, n, experts, ls, k,
-          N.GRZ_NORMALIZE if normalize else 0, _list(ids, "ids", dev, _I32, n, k),
-          _list(weights, "weights", dev, _F32, n, k))
+          N.GRZ_NORMALIZE if normalize else 0, ip, _list(weights, "weights", dev, _F32, n, k))
 
 
 def dp_expert_route_grad(logits, ids, dweights, dlogits, normalize=False, stream=None):
@@ -58,10 +62,10 @@ def dp_expert_route_grad(logits, ids, dweights, dlogits, normalize=False, stream
     listed ``ids``.  ``dlogits`` may be ``logits`` itself."""
     dev = _device(logits, "logits")
     lp, lt, n, experts, ls = _rows(logits, "logits", dev)
-    k = _slots(ids, "ids")[1]
+    ip, k = _slots(ids, "ids", dev, _I32, n)
     gp, _, _, _, gs = _rows(dlogits, "dlogits", dev, n, experts, logits.dtype)
     _call("dp_expert_route_grad", dev, stream, lp, lt, n, experts, ls, k,
-          N.GRZ_NORMALIZE if normalize else 0, _list(ids, "ids", dev, _I32, n, k),
+          N.GRZ_NORMALIZE if normalize else 0, ip,
           _list(dweights, "dweights", dev, _F32, n, k), gp, gs)
 
 
@@ -77,7 +81,9 @@ def dp_expert_sort(ids, experts, offsets, places, workspace=None, stream=None):
     ``experts + 1``).  ``workspace``: ``dp_expert_sort_workspace`` bytes of any type,
     4-byte aligned, or None where it needs none."""
     dev = _device(ids, "ids")
-    n, k = _slots(ids, "ids")
+    if ids.dim() != 2:
+        raise ValueError(f"ids has shape {tuple(ids.shape)}, expected tokens x slots")
+    n, k = ids.shape
     ip, bits = _ids(ids, "ids", dev, n, k)
     need = dp_expert_sort_workspace(n, k, experts)
     ws = None
@@ -96,17 +102,12 @@ def dp_expert_sort(ids, experts, offsets, places, workspace=None, stream=None):
           _list(places, "places", dev, _I32, n, k))
 
 
-def _places(places, dev, n):
-    k = _slots(places, "places")[1]
-    return _list(places, "places", dev, _I32, n, k), k
-
-
 def dp_expert_dispatch(x, places, out, weights=None, stream=None):
     """``out[places[i, j]] = weights[i, j] * x[i]`` (``x[i]`` without weights); rows
     that no place names are left as they were."""
     dev = _device(x, "x")
     xp, xt, n, dim, xs = _rows(x, "x", dev)
-    pp, k = _places(places, dev, n)
+    pp, k = _slots(places, "places", dev, _I32, n)
     op, ot, rows, _, os_ = _rows(out, "out", dev, None, dim)
     _call("dp_expert_dispatch", dev, stream, xp, xt, xs, pp,
           _list(weights, "weights", dev, _F32, n, k), n, k, dim, rows, op, ot, os_)
@@ -119,7 +120,7 @@ def dp_expert_combine(y, places, out, weights=None, accumulate=False, stream=Non
     dev = _device(y, "y")
     yp, yt, rows, dim, ys = _rows(y, "y", dev)
     op, ot, n, _, os_ = _rows(out, "out", dev, None, dim)
-    pp, k = _places(places, dev, n)
+    pp, k = _slots(places, "places", dev, _I32, n)
     _call("dp_expert_combine", dev, stream, yp, yt, ys, rows, pp,
           _list(weights, "weights", dev, _F32, n, k), n, k, dim,
           N.GRZ_ACCUMULATE if accumulate else 0, op, ot, os_)
@@ -132,7 +133,7 @@ def dp_expert_combine_grad(dout, y, places, weights, dy=None, dweights=None, str
     ``y`` None where ``dweights`` is."""
     dev = _device(dout, "dout")
     dp, dt, n, dim, ds = _rows(dout, "dout", dev)
-    pp, k = _places(places, dev, n)
+    pp, k = _slots(places, "places", dev, _I32, n)
     if y is not None:
         yp, yt, rows, _, ys = _rows(y, "y", dev, None, dim)
     elif dweights is not None or dy is None:
