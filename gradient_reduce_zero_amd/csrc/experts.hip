@@ -34,7 +34,8 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // ---------------------------------------------------------------------------
 // Vectors of a row that begin anywhere: gfx950 reads and writes 8 and 16 bytes at
 // any element's address, so rows need no alignment of their own (8000 x 1601 bf16 to
-// 4 experts, every row off the borders: 35.7 us for 128 MB, sort included).
+// 4 experts, every row off the lines: 36 us for 128 MB, sort included, and back 25;
+// 8000 x 1600 27 and 22).  Vectors shifted onto each row's own lines were slower.
 
 // N consecutive elements as they lie in memory (8 or 16 bytes), widened one by one
 // where they are used: many loads wait in few registers.
@@ -540,17 +541,18 @@ __global__ __launch_bounds__(kSortThreads) void expert_place_kernel(SortArgs a) 
 // Bound by HBM, and by what 64 experts' rows written side by side cost it: 16384 x
 // 4096 bf16 to 6 experts of 64 147-160 us, 5.9-6.4 TB/s (places in the tokens' order
 // 8 % less).  Small workgroups free their slots one by one: 174 us a call with two waves,
-// 177 with four, 185 with eight; two or four vectors a lane 192 and 195.
-constexpr int kDispatchWaves = 2;
-
-template <typename TI, typename TO>
-__global__ __launch_bounds__(kDispatchWaves * 64) void dispatch_kernel(
+// 175 with four, 186 with eight; two or four vectors a lane 192 and 195.  Where rows lie
+// off the lines, neighbouring waves write halves of one, which have to meet in one L2, so
+// in one workgroup: 16384 x 2056 fp32 to 3 bf16 rows 91 us with two waves, 80 with four,
+// 75 with eight; 4000 x 4097 bf16 to 8 83, 76 and 74.
+template <typename TI, typename TO, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void dispatch_kernel(
     const TI* __restrict__ x, int64_t xstride, const int32_t* __restrict__ places,
     const float* __restrict__ weights, int64_t row0, int64_t n, int k, int64_t dim, int parts,
     int64_t rows, TO* __restrict__ out, int64_t ostride) {
   constexpr int VEC = cols_of<TI, TO>();
   const int lane = threadIdx.x & 63;
-  const auto [token, run] = unit_of<kDispatchWaves>(row0, parts);
+  const auto [token, run] = unit_of<WAVES>(row0, parts);
   if (token >= n) return;
   const TI* src = x + token * xstride;
   const int64_t whole = dim - dim % VEC;
@@ -821,11 +823,12 @@ int dispatch_run(const void* x, int64_t xstride, const int32_t* places, const fl
                  int64_t n, int k, int64_t dim, int64_t rows, void* out, int64_t ostride,
                  hipStream_t stream) {
   const int parts = static_cast<int>(ceil_div(dim, 64 * cols_of<TI, TO>()));
+  const bool on_lines = aligned(out, 128) && ostride * static_cast<int64_t>(sizeof(TO)) % 128 == 0;
+  const int waves = on_lines ? 2 : 8;
   return in_batches(n, ceil_div(kUnitBatch, parts), [&](int64_t tokens, int64_t r) {
-    return launch(dispatch_kernel<TI, TO>,
-                  dim3(static_cast<unsigned>(ceil_div(tokens * parts, kDispatchWaves))),
-                  dim3(kDispatchWaves * 64), stream,
-                  static_cast<const TI*>(x), xstride, places, weights, r,
+    return launch(on_lines ? dispatch_kernel<TI, TO, 2> : dispatch_kernel<TI, TO, 8>,
+                  dim3(static_cast<unsigned>(ceil_div(tokens * parts, waves))), dim3(64 * waves),
+                  stream, static_cast<const TI*>(x), xstride, places, weights, r,
                   std::min(n, r + tokens), k, dim, parts, rows, static_cast<TO*>(out), ostride);
   });
 }

@@ -749,8 +749,8 @@ int dp_distill_grad(const void* logits, int dtype, int64_t n, int64_t vocab, int
  * dweights = dp_expert_combine_grad(dout = x, y = drows) without dy.)
  *
  * Shared conventions: row matrices, sizes, arithmetic and errors as for the
- * operators addressed by token ids (rows at any element's address are about as
- * fast as those on 16-byte borders), and
+ * operators addressed by token ids (rows on 128-byte lines are fastest; others, at
+ * any element's address, take 10 to 30 % longer), and
  *
  *  - Slots.  A token has k of them (1..GRZ_MAX_SLOTS), slot j of token i at index
  *    i * k + j of the contiguous n x k arrays.  n * k is at most 2^28, columns at
