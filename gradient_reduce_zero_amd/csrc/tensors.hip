@@ -537,7 +537,8 @@ int dp_grad_sqnorm_tensors(const grz_tensor* tensors, int64_t count, double max_
     if (k == 0) continue;
     st = k <= kFewPieces
              ? launch(tensors_norm_few_kernel, dim3(k), dim3(256), stream, a)
-             : launch(bytes >= kStreamBytes ? tensors_norm_kernel<true> : tensors_norm_kernel<false>,
+             : launch(bytes >= kStreamBytes ? tensors_norm_kernel<true>
+                                            : tensors_norm_kernel<false>,
                       dim3(static_cast<unsigned>(ceil_div(k, 4))), dim3(256), stream, a);
     if (st != GRZ_OK) return st;
     a.pieces += k;

@@ -247,7 +247,8 @@ def test_binding_refuses_what_the_library_cannot_see():
 def test_layouts_of_a_list():
     from gradient_reduce_zero_amd.tensors import _one_run
     a = torch.zeros(6, 5, 4)
-    for t in (a, a.permute(2, 0, 1), a.transpose(0, 1), a[2:3].transpose(0, 2), torch.zeros(3).expand(1, 3)):
+    for t in (a, a.permute(2, 0, 1), a.transpose(0, 1), a[2:3].transpose(0, 2),
+              torch.zeros(3).expand(1, 3)):
         assert _one_run(t)
     for t in (a[:, :3], a[::2], a[:1].expand(6, 5, 4), a[..., 0], torch.zeros(1).expand(2)):
         assert not _one_run(t)

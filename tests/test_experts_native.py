@@ -35,8 +35,9 @@ def test_host_code_under_address_sanitizer(tmp_path):
           f"-I{INC}", EXPERTS_SRC, TENSORS_SRC, "-o", str(lib)])
     exe = tmp_path / "experts_host_checks_asan"
     rt = _asan_runtime()
-    _run([f"{ROCM}/llvm/bin/clang", "-g", "-O1", "-fsanitize=address", "-shared-libsan", *INCLUDES,
-          "-DWITHOUT_STEP", "-rdynamic", SRC, f"-L{tmp_path}", "-lexperts", f"-Wl,-rpath,{tmp_path}",
-          f"-Wl,-rpath,{ROCM}/lib", f"-Wl,-rpath,{rt}", "-o", str(exe)])
+    _run([f"{ROCM}/llvm/bin/clang", "-g", "-O1", "-fsanitize=address", "-shared-libsan",
+          *INCLUDES, "-DWITHOUT_STEP", "-rdynamic", SRC, f"-L{tmp_path}", "-lexperts",
+          f"-Wl,-rpath,{tmp_path}", f"-Wl,-rpath,{ROCM}/lib", f"-Wl,-rpath,{rt}",
+          "-o", str(exe)])
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=0:abort_on_error=0")
     assert PASSED in _run([str(exe)], env=env).stdout

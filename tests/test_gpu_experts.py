@@ -13,6 +13,7 @@ from token_ref import assert_close
 
 pytestmark = pytest.mark.gpu
 I32 = torch.int32
+U_ROW = 2.0 ** -24  # half a step of fp32
 LAYOUTS = [(0, 0), (8, 8), (3, 1)]  # elements between rows, and before the first
 
 
@@ -332,6 +333,55 @@ def test_weights_of_zero_infinity_and_nan():
     want, tol = ref.combine(y, places, w)
     assert_close(out, want, tol, "combine")
     assert torch.isnan(out[0, 3]) and torch.isnan(out[0, 5]) and out[1, 7] == math.inf
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_gradients_against_differences(weighted):
+    # The sum <g, combine(y, w)> is linear in y and in w, <G, dispatch(x)> in x: central
+    # differences of the 64-bit forms along a direction are exact but for their own
+    # roundings (1e-9 of the magnitudes here), so only the kernels' bounds remain.
+    n, k, d, h = 30, 3, 45, 0.5
+    places, w = slots_of(n, k, n * k - 7, 52)
+    w = torch.nan_to_num(w) if weighted else None
+    rows = n * k - 7
+    y, _ = matrix(rows, d, F32, seed=53)
+    g, _ = matrix(n, d, F32, seed=54)
+    x, _ = matrix(n, d, F32, seed=55)
+    dy, dw = torch.zeros_like(y), torch.empty(n, k, device=DEV)
+    grz.dp_expert_combine_grad(g, y, places, w, dy=dy, dweights=dw)
+    dx = torch.empty_like(x)
+    grz.dp_expert_combine(y, places, dx, weights=w)       # y in the place of the rows' gradient
+    gd, yd = g.double().cpu(), y.double().cpu()
+    ones = torch.ones(n, k, dtype=torch.float64)
+    wd = ones if w is None else w.double().cpu()
+    rand = torch.Generator().manual_seed(56)
+    ok, at = ref.live(places, rows)
+    reached = torch.zeros(rows, dtype=torch.bool)
+    reached[at[ok]] = True
+
+    def slope(loss, point, move):
+        return (loss(point + h * move) - loss(point - h * move)) / (2 * h)
+
+    def loss_y(t):
+        return (gd * ref.combine(t, places, wd)[0]).sum()
+
+    def loss_w(t):
+        return (gd * ref.combine(yd, places, t)[0]).sum()
+
+    def loss_x(t):  # rows of a dispatch against y
+        return sum(((wd[i, j] * t[i]) * yd[at[i, j]]).sum() for i, j in ok.nonzero().tolist())
+
+    for loss, point, got, bound in (
+            (loss_y, yd, dy, U_ROW * dy.abs()),
+            (loss_w, wd, dw, ref.combine_grad(g, y, places, w, torch.zeros_like(y))[2]),
+            (loss_x, x.double().cpu(), dx, ref.combine(y, places, w)[1])):
+        move = torch.randn(point.shape, generator=rand, dtype=torch.float64)
+        want = slope(loss, point, move)
+        got = got.double().cpu()
+        terms = (got * move).abs()
+        lim = ((bound.double().cpu() + U_ROW * got.abs()) * move.abs()).sum() + 1e-9 * terms.sum()
+        assert abs((got * move).sum() - want) <= lim
+    assert (dy.cpu()[~reached] == 0).all()
 
 
 # -- large offsets, batches of launches, streams, graphs ------------------------------------

@@ -233,7 +233,8 @@ def test_orders_of_dimensions_and_refused_layouts():
         with pytest.raises(ValueError, match="apart"):
             grz.TensorList([bad])
     with pytest.raises(ValueError, match="strides"):
-        grz.dp_grad_clip_tensors([a], None, out=[torch.empty(5, 40, 30, device=DEV).permute(2, 1, 0)])
+        grz.dp_grad_clip_tensors([a], None,
+                                 out=[torch.empty(5, 40, 30, device=DEV).permute(2, 1, 0)])
     with pytest.raises(ValueError, match="shape"):
         grz.dp_grad_clip_tensors([a], None, out=[torch.empty(30, 200, device=DEV)])
     with pytest.raises(ValueError):
