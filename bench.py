@@ -194,6 +194,13 @@ def _oracle_worker(i, count, n, rank, chunk, wire, divisor, barrier, results):
         results.put(("error", i, repr(e), 0.0, 0.0))
 
 
+def _first_failure(reports):
+    """The failed report to quote, or None: a worker's own error before the broken
+    barrier it causes in the others, whose reports may arrive first."""
+    bad = [r for r in reports if r[0] != "ok"]
+    return min(bad, key=lambda r: r[2].startswith("BrokenBarrierError"), default=None)
+
+
 def cpu_baseline_parallel(count, n, rank, chunk, workers, wire=None, divisor=None):
     """The same oracle step over ``count`` parameters split into ``workers``
     disjoint tiles, one forked process each, all started together.  Runs
@@ -228,9 +235,9 @@ def cpu_baseline_parallel(count, n, rank, chunk, workers, wire=None, divisor=Non
             if not ok and pr.is_alive():
                 pr.kill()  # our own children, by handle
             pr.join(timeout=60)
-    bad = [r for r in got if r[0] != "ok"]
+    bad = _first_failure(got)
     if bad:
-        raise RuntimeError(f"oracle worker {bad[0][1]} failed: {bad[0][2]}")
+        raise RuntimeError(f"oracle worker {bad[1]} failed: {bad[2]}")
     t0, t1 = min(r[3] for r in got), max(r[4] for r in got)
     return dict(value=count / (t1 - t0), unit="params/s", cores=workers, kind="oracle",
                 seconds=t1 - t0,
