@@ -8,9 +8,14 @@ of them) and the tensors' join them, so that one clip factor counts both::
     grads = TensorList([p.grad for p in experts])
     ws = torch.empty(dp_grad_sqnorm_tensors_workspace(grads, lead) // 8,
                      dtype=torch.float64, device=dev)
-    ws[:lead].copy_(norm.partials)            # from dp_reduce_scatter_mean
+    dp_reduce_scatter_mean(arenas, buckets, chunk, mean, ws[:lead])
     dp_grad_sqnorm_tensors(grads, max_norm, ws, sqnorm, scale, lead=lead)
+    zero1_adamw_gather(w, m, v, mean, buckets, nranks, chunk, scale, args, replicas)
     dp_grad_clip_tensors(grads, scale)
+
+The factor has to be there before the arena's update; the step drivers form their
+own, of the arena alone.  AdamW applies the factor it is given, so fp32 gradients that go
+through ``zero1_adamw_step`` need no clip of their own.
 
 As in the rest of the binding the caller owns every buffer, the work is enqueued on
 the current stream of the tensors' device (or ``stream``), and nothing synchronises

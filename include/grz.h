@@ -891,7 +891,8 @@ size_t dp_grad_sqnorm_tensors_workspace(const grz_tensor* tensors, int64_t count
  * workspace  device, dp_grad_sqnorm_tensors_workspace bytes, 8-byte aligned.  Its
  *            first `lead` doubles are the sums that are there; on return the
  *            list's dp_tensor_pieces follow them.  Calls that may run at the same
- *            time need one each.
+ *            time need one each.  The pieces' order decides the sum's last bits:
+ *            ranks that want the same ones fold all ranks' pieces in one order.
  * max_norm, sqnorm_out, clip_scale_out  as for dp_grad_sqnorm (either output may be
  *            NULL, not both).  A tensor listed twice counts twice.
  */
