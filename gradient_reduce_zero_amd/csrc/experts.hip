@@ -11,7 +11,9 @@
 // All are bound by HBM or, where small, by their launches: at most three flops
 // per byte (the router apart, which its instructions bound).  Integer atomics in LDS
 // only, so every result bit is the same from run to run.  Times below are of one
-// MI355X.
+// MI355X, on three sets of inputs in turn unless a comment says one set (whose rows the
+// caches then hold): of a kernel in a trace or a replayed graph of its calls, which agree
+// within 0.6 us, or of a call from Python among others, where it says call.
 
 #include <hip/hip_runtime.h>
 
@@ -119,8 +121,8 @@ template <int WAVES> __device__ __forceinline__ Unit unit_of(int64_t row0, int p
 // four rows to a wave, or 64), V in each, so that every maximum and sum is V
 // operations and four (or six) lane exchanges.  The k largest come one at a time: the
 // row's largest key, the lowest element that has it, which is then taken out.  Bound by
-// those rounds' instructions: 16384 x 128 bf16, k = 8: 5.4 us for 5 MB; 16384 x 256: 7.1
-// us bf16, 9.0 fp32.
+// those rounds' instructions (V a round, so k V): normalized, k = 8, 16384 x 128 bf16 5.8
+// us for 5 MB, fp32 6.8; 16384 x 256 7.8 and 10.8; 0.3 to 0.7 more not normalized.
 
 // Keys ordered as the logits are: larger for larger, NaN above all, -0 as 0, and 0
 // for an element that is not there or taken out.
@@ -137,7 +139,8 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 }
 // A bf16 value's key is its upper half (the lower half is 0, or 0xffff below zero, and
 // is restored from its sign), which leaves room for the element's number, lower ones
-// first: one maximum then finds both (16384 x 256 bf16, k = 8: 9.2 us without).
+// first: one maximum then finds both (16384 x 256 bf16, k = 8, one set: 9.2 us without,
+// 7.7 with).
 __device__ __forceinline__ uint32_t numbered(uint32_t key, int number) {
   return (key & 0xffff0000u) | (0xffffu - static_cast<uint32_t>(number));
 }
@@ -195,8 +198,8 @@ __device__ __forceinline__ float weight_of(float x, float m) {
 
 // Which of the row's elements a lane of the group holds: runs of `kRun` (one access),
 // the group's runs side by side, so that each access of a wave is one run of memory a
-// row (with V consecutive elements a lane the gradient of 16384 x 256 took 7.6 us bf16
-// and 14.9 fp32, instead of 6.1 and 6.4).
+// row (with V consecutive elements a lane the gradient of 16384 x 256, one set, took 7.6
+// us bf16 and 14.9 fp32, instead of 6.1 and 6.4).
 template <typename T, int G, int V> struct Share {
   static constexpr int kRun = V == 1 ? 1 : sizeof(T) == 2 && V >= 8 ? 8 : 4;
   int g;
@@ -325,7 +328,7 @@ __global__ __launch_bounds__(256) void route_kernel(const T* __restrict__ logits
 // LDS, where each lane finds those of its elements; a token that lists an expert
 // twice has both slots add theirs up first, in the slots' order.  Normalized weights
 // depend on the listed logits alone, so only those are read.  16384 x 256 bf16, k = 8:
-// 6.1 us, 7.4 not normalized (17 MB).
+// 6.8 us, 8.4 not normalized (17 MB); fp32 7.3 and 10.9.
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void route_grad_kernel(
     const T* logits, int64_t stride, int64_t row0, int64_t n, int experts, int k, bool normalize,
@@ -401,13 +404,22 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
 // it, and `before` those of the tiles before its own.
 //
 //  - up to kDirectSlots one launch: each workgroup counts all slots itself, those
-//    before its tile and all, with integer atomics in LDS (4096 slots of 64 experts
-//    4.9 us, 8192 5.8 against 6.8 by the next one, 16384 7.5 against 7.0; of 8 experts,
-//    whose counts collide more, 7.0 against 6.5 and 10.5 against 6.5);
+//    before its tile and all, with integer atomics in LDS;
 //  - beyond that the tiles are counted by a first launch and each workgroup adds all
-//    tiles' counts up (98304 slots of 64 experts 8.3 us).  At most kMaxTiles tiles, and
-//    at most kTileCounts counts, since everyone reads them (524288 slots of 1024
-//    experts: 24.6 us, 28.2 with 256 tiles, 30.7 with 64).
+//    tiles' counts up (98304 slots of 64 experts 8.7 us: 2.4 and 6.4 in a trace, 4.8 and
+//    6.0 where the ids come from HBM).  At most kMaxTiles tiles, and at most kTileCounts
+//    counts, since everyone reads them (524288 slots of 1024 experts: 24.6 us, 28.2 with
+//    256 tiles, 30.7 with 64).
+//
+// One launch and two, us, ids spread evenly:
+//   slots    of 2          8          64         1024 experts   all of one of 64
+//   4096     7.6  7.5   5.8  6.9   5.4  7.1   6.5  9.3      10.4  7.5
+//   8192    11.5  7.5   7.5  7.0   6.2  7.2   7.3  9.0      17.3  7.7
+//   16384   19.5  7.6  10.9  7.0   7.8  7.4   9.0  9.5      30.9  7.8
+// The lanes of a wave add to one count one after the other, so few experts, or ids that
+// are much alike, make the one launch slow.  The limit takes the slots alone: at
+// 8192 of them it loses 0.5 us with 8 experts and saves 1.0 with 64, and how alike the
+// ids are is known on the device only.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
@@ -748,8 +760,8 @@ template <typename F> int in_batches(int64_t n, int64_t batch, F f) {
 }
 
 // Lanes to a row and logits to a lane.  Sixteen lanes up to 256 experts and 16
-// slots: four rows share a wave's instructions (16384 x 512 rows, which do not, take
-// 13.9 us where 256 take 7.1).
+// slots: four rows share a wave's instructions (16384 x 512 bf16, which do not, take
+// 15.1 us where 256 take 7.6).
 #define GRZ_ROUTE_SHAPES(CALL)               \
   if (k <= 16 && experts <= 16) CALL(16, 1)  \
   if (k <= 16 && experts <= 64) CALL(16, 4)  \
@@ -847,10 +859,17 @@ int combine_run(const void* y, int64_t ystride, int64_t rows, const int32_t* pla
                     std::min(n, r + tokens), k, dim, parts, static_cast<TO*>(out), ostride);
     });
   };
-  // Vectors a lane: one while that gives the chip few waves (32 x 4096 bf16, k = 8: 3.7 us
-  // with one, 5.2 with four; 1024 x 4096: 12.4 and 13.3), more of them then spare
-  // instructions (4096 x 768 bf16, k = 4: 5.5 us with one, 4.9 with two; 16384 x
-  // 4096, k = 6: 162 with one, 155 with four).
+  // Vectors a lane: one while that gives the chip few waves, up to 2048, and up to 8192
+  // where more than four rows are on their way in each.  us with one, two and four, bf16,
+  // waves with one in brackets: 256 x 4096 from 4 (2048) 4.0, 4.3, 4.9; 512 x 4096 from 4
+  // (4096) 5.9, 6.0, 6.4; 4096 x 768 from 4 (8192) 7.2, 7.2, 7.8; 1024 x 4096 from 8
+  // (8192) 13.4, 14.2, 15.2; 8192 x 768 from 8 (16384) 21.6, 20.6, 23.8; 2048 x 4096 from
+  // 8 (16384) 28.8, 26.9, 27.4.
+  // Then two, or four from rows of eight on, where the two are close: 8000 rows from 4,
+  // 2048 columns 30.9, 28.4, 28.7; 3584 51.6, 47.7, 49.1; 4096 58.5, 54.6, 55.6; 6144
+  // 86.7, 81.2, 81.2; 8192 116, 111, 107; fp32 1600 columns 45.9, 42.3, 43.0; 2048 58.3,
+  // 53.8, 54.0; 4096 115, 109, 106.  16384 x 4096 bf16 from 6: 171, 161, 157.  (Worst for
+  // four: 8000 x 2560 fp32 from 2, 40.3 with two, 42.2.)
   const int64_t units = n * ceil_div(dim, 64 * VEC);
   const bool past = n * k * dim * static_cast<int64_t>(sizeof(TI)) >= kStreamBytes;
   const bool wide = dim >= 8 * 64 * VEC;
@@ -879,8 +898,12 @@ int combine_grad_run(const void* dout, int64_t dstride, const void* y, int64_t y
                     std::min(n, r + tokens), k, dim, static_cast<TY*>(dy), dystride, dweights);
     });
   };
-  // Eight vectors a lane for rows that fill them (16384 x 4096 bf16, k = 6: 321 us, 326
-  // with four; 8000 x 1601, k = 4: 56 and 48).
+  // Eight vectors a lane for rows that four do not hold, which so read them in one
+  // pass; a row that four hold leaves half of eight idle.  us with four and eight, 8000
+  // rows from 4, bf16: 1601 columns 49 and 57, 2048 49.5 and 51.3; 2056 58.5 and 57.0,
+  // 2304 56.6 and 57.7, 2560 62.8 and 62.3, 3080 84.7 and 80.4, 4096 100.0 and 98.2, 8192
+  // 225 and 221; fp32: 1024 50.0 and 50.8; 1032 59.2 and 57.2, 1280 62.8 and 62.3, 1601
+  // 91.0 and 85.7, 2048 99.3 and 97.0.
   const bool wide = dim > 4 * 64 * cols_of<TD, TY>();
   if (n * k * dim * static_cast<int64_t>(sizeof(TY)) >= kStreamBytes)
     return wide ? go(combine_grad_kernel<TD, TY, 8, true>)

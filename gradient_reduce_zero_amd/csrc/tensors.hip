@@ -309,9 +309,9 @@ __global__ __launch_bounds__(256) void tensors_norm_few_kernel(const NormArgs a)
 
 // ---------------------------------------------------------------------------
 // Scaling: a one-wave workgroup to a run of a piece, which leaves its CU as soon as its
-// own few accesses are done.  Bound by HBM: 1.04 G bf16 elements 660 us, 6.3 TB/s (four
-// waves 682; runs of 512 elements 736, of 2048 672, of 4096 708); 10.6 M, from the
-// caches in part: 10.2 us, 9.5 with runs of 2048.
+// own few accesses are done.  Bound by HBM: 1.04 G bf16 elements 660 us, 6.3 TB/s (676 in
+// a trace of its two launches; four waves 682; runs of 512 elements 736, of 2048 672, of
+// 4096 708); 10.6 M, from the caches in part: 10.2 us, 9.5 with runs of 2048.
 
 template <bool STREAM> constexpr int kRun = STREAM ? 1024 : 2048;  // elements
 
